@@ -51,6 +51,10 @@ typedef enum {
     S4_ERR_CUDA = 4          /* a CUDA runtime call or launch failed */
 } s4_status;
 
+/* Element types of the token-major operators (layer norm over rows, gated
+ * delta rule). 16-bit values are computed with in float and rounded once. */
+typedef enum { S4_F32 = 0, S4_BF16 = 1, S4_F16 = 2 } s4_dtype;
+
 /* Bits OR-ed into *d_flags by the kernels. */
 #define S4_FLAG_UNSTABLE  1u  /* some Re(Lambda) >= 0 (or Re(a) >= 0 for S4D)   */
 #define S4_FLAG_NONFINITE 2u  /* a non-finite value was produced                 */
@@ -62,6 +66,8 @@ typedef enum {
 #define S4_MAX_NH 256       /* stored modes per channel                          */
 #define S4_MAX_H 65535      /* channels per call (kernel and decode entry points) */
 #define S4_MAX_DENSE_N 128  /* full state size of the dense decode step           */
+#define S4_MAX_DELTA_D 128  /* key and value head size of the gated delta rule    */
+
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *s4_status_string(s4_status s);
@@ -562,6 +568,78 @@ s4_status s4_recurrent_step(s4_step_mode mode, const s4_c32 *Abar, const s4_c32 
 s4_status s4_recurrent_scan(s4_step_mode mode, const s4_c32 *Abar, const s4_c32 *Bbar,
                             const s4_c32 *C, const float *D, int Bt, int H, int Ns, int T,
                             s4_c32 *x, const float *u, float *y, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm over token rows: x, z [rows, D] of the given element type, row
+ * major and contiguous, gamma and beta [D] float.
+ *
+ * s4_layernorm: z[r,c] = (x[r,c] - mean[r]) * rstd[r] * gamma[c] + beta[c],
+ *   mean and the biased variance of the row in float, rstd = 1 / sqrt(var +
+ *   eps). mean, rstd [rows] float out (the backward pass reads them). z may
+ *   equal x (but the backward pass needs x).
+ *
+ * s4_layernorm_backward: with xhat = (x - mean) rstd and h = dz gamma,
+ *     dx = rstd (h - mean_c(h) - xhat mean_c(h xhat)),
+ *     dgamma = sum_r dz xhat,  dbeta = sum_r dz   ([D] float out).
+ *   dx may equal dz. The sums over rows are taken in float in a fixed order:
+ *   the same inputs give the same bits.
+ *
+ * s4_layernorm_channels_backward: the same for s4_layernorm_channels: dz, x,
+ *   dx [Bt, H, L] float, the norm over H at each (b, t) (mean and variance
+ *   are computed again from x), dgamma and dbeta summed over (b, t).
+ *
+ * workspace: s4_layernorm_backward_workspace_size(D) bytes (D = H for the
+ * channels), device, 256-byte aligned, free again once the call has run.
+ * 0 <= rows < 2^31 (no rows: nothing is written but zero weight gradients),
+ * 1 <= D <= 8192; 16-byte aligned rows are read 16 bytes at a time, others
+ * element by element.
+ * Errors: null pointers, eps <= 0 or not finite, pointers not aligned to
+ * their element (16 bytes for the channels), overlaps other than those named
+ * -> S4_ERR_INVALID_ARG; D, rows or L out of range -> S4_ERR_UNSUPPORTED;
+ * workspace too small or misaligned -> S4_ERR_WORKSPACE.
+ * ------------------------------------------------------------------------ */
+s4_status s4_layernorm(s4_dtype dtype, const void *x, const float *gamma, const float *beta, float eps,
+                       long long rows, int D, void *z, float *mean, float *rstd, cudaStream_t stream);
+
+s4_status s4_layernorm_backward_workspace_size(int D, size_t *bytes);
+
+s4_status s4_layernorm_backward(s4_dtype dtype, const void *dz, const void *x, const float *gamma,
+                                const float *mean, const float *rstd, long long rows, int D, void *dx,
+                                float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+s4_status s4_layernorm_channels_backward(const float *dz, const float *x, const float *gamma, float eps, int Bt,
+                                         int H, int L, float *dx, float *dgamma, float *dbeta, void *workspace,
+                                         size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The gated delta rule: a recurrence like s4_recurrent_step's whose decay and
+ * writes depend on the input. Per value head, with state S [Dk, Dv] (float):
+ *     S_t = a_t S_{t-1} + k_t u_t^T,  a_t = exp(g_t),
+ *     u_t = beta_t (v_t - a_t S_{t-1}^T k_t),  o_t = scale S_t^T q_t.
+ * Value head h reads key head h / (Hv / Hk); Hv is a multiple of Hk.
+ *   q, k : [Bt, T, Hk, Dk], v, o : [Bt, T, Hv, Dv] of the given element type;
+ *   heads and elements contiguous, q_stride, k_stride and v_stride elements
+ *   between tokens (Hk Dk, Hk Dk and Hv Dv when contiguous; larger when they
+ *   are slices of one projection), o contiguous. g, beta : [Bt, T, Hv] float.
+ *   state : [Bt, Hv, Dk, Dv] float. q, k, v, o and states 16-byte aligned,
+ *   strides a multiple of 16 bytes.
+ *   Dk, Dv multiples of 8 up to 128. g <= 0 and keys of norm <= 1 keep the
+ *   recurrence stable; neither is checked. g = -inf clears the state. Sums,
+ *   states and gates are float.
+ *
+ * s4_gated_delta_scan runs T >= 0 tokens of each sequence one after the other
+ *   (T = 1: a decode step), the state in place. Bound by reading and writing
+ *   the states: for many tokens s4_gated_delta_forward is the faster form.
+ * Errors: null pointers, sizes < 1, Hv not a multiple of Hk, misalignment,
+ * strides too small, overlap of an output with another operand, scale not
+ * finite -> S4_ERR_INVALID_ARG; Dk or Dv not a multiple of 8 or above 128
+ * -> S4_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------ */
+s4_status s4_gated_delta_scan(s4_dtype dtype, const void *q, long long q_stride, const void *k, long long k_stride,
+                              const void *v, long long v_stride, const float *g, const float *beta, float scale,
+                              float *state, int Bt, int T, int Hk, int Hv, int Dk, int Dv, void *o,
+                              cudaStream_t stream);
 
 #ifdef __cplusplus
 }

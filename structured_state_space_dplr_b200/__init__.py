@@ -27,6 +27,8 @@ __all__ = [
     "S4_STEP_DIAG", "S4_STEP_DPLR", "dplr_discretize_structured", "dplr_ctilde", "forward_dplr_host",
     "fft_conv_host", "fft_conv_apply_adjoint", "fft_conv_kernel_grad", "fft_conv_kernel_grad_workspace_size",
     "kernel_dplr_backward", "kernel_dplr_backward_workspace_size", "s4d_kernel_vandermonde_backward", "load",
+    "layernorm", "layernorm_backward", "layernorm_backward_workspace_size", "layernorm_channels_backward",
+    "gated_delta_step", "gated_delta_scan",
 ]
 
 
@@ -589,3 +591,155 @@ def recurrent_scan(Abar, Bbar, C, D, x, u, *, out=None, mode=None):
     _lib.call("s4_recurrent_scan", mode, _ptr(Abar), _ptr(Bbar), _ptr(C), _ptr(D), Bt, H, Ns, T,
               _ptr(x), _ptr(u), _ptr(out), _stream())
     return out
+
+
+# ------------------------------------------- token-major operators ----
+_DTYPES = {torch.float32: _lib.S4_F32, torch.bfloat16: _lib.S4_BF16, torch.float16: _lib.S4_F16}
+
+
+def _dtype(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be a float32, bfloat16 or float16 tensor")
+    return _DTYPES[t.dtype]
+
+
+def _buffer(t, name, shape, dtype, device):
+    """t, checked, or a new tensor where it is None."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _cuda(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def layernorm(x, gamma, beta, eps=1e-5, *, out=None, mean=None, rstd=None):
+    """Layer norm over the last axis of x [..., D] (float32, bfloat16 or
+    float16; gamma, beta [D] float32; s4_layernorm). Returns (z, mean, rstd):
+    z of x's type, mean and rstd [...] float32 for layernorm_backward. out may
+    be x."""
+    kind = _dtype(x, "x")
+    _cuda(x, "x")
+    D = x.shape[-1]
+    _buffer(_cuda(gamma, "gamma"), "gamma", (D,), torch.float32, x.device)
+    _buffer(_cuda(beta, "beta"), "beta", (D,), torch.float32, x.device)
+    out = _buffer(out, "out", x.shape, x.dtype, x.device)
+    mean = _buffer(mean, "mean", x.shape[:-1], torch.float32, x.device)
+    rstd = _buffer(rstd, "rstd", x.shape[:-1], torch.float32, x.device)
+    _lib.call("s4_layernorm", kind, _ptr(x), _ptr(gamma), _ptr(beta), float(eps), mean.numel(), D, _ptr(out),
+              _ptr(mean), _ptr(rstd), _stream())
+    return out, mean, rstd
+
+
+def layernorm_backward_workspace_size(D) -> int:
+    """Bytes of workspace layernorm_backward (or, with D = H,
+    layernorm_channels_backward) needs."""
+    n = ctypes.c_size_t(0)
+    _lib.call("s4_layernorm_backward_workspace_size", int(D), ctypes.byref(n))
+    return n.value
+
+
+def _norm_workspace(D, device, workspace):
+    if workspace is None:
+        workspace = torch.empty(layernorm_backward_workspace_size(D), dtype=torch.uint8, device=device)
+    return _cuda(workspace, "workspace", torch.uint8)
+
+
+def layernorm_backward(dz, x, gamma, mean, rstd, *, dx=None, dgamma=None, dbeta=None, workspace=None):
+    """Backward of layernorm (s4_layernorm_backward): returns (dx of x's type,
+    dgamma, dbeta [D] float32). dx may be dz."""
+    kind = _dtype(x, "x")
+    _cuda(x, "x")
+    D = x.shape[-1]
+    _buffer(_cuda(dz, "dz"), "dz", x.shape, x.dtype, x.device)
+    _buffer(_cuda(gamma, "gamma"), "gamma", (D,), torch.float32, x.device)
+    _buffer(_cuda(mean, "mean"), "mean", x.shape[:-1], torch.float32, x.device)
+    _buffer(_cuda(rstd, "rstd"), "rstd", x.shape[:-1], torch.float32, x.device)
+    dx = _buffer(dx, "dx", x.shape, x.dtype, x.device)
+    dgamma = _buffer(dgamma, "dgamma", (D,), torch.float32, x.device)
+    dbeta = _buffer(dbeta, "dbeta", (D,), torch.float32, x.device)
+    workspace = _norm_workspace(D, x.device, workspace)
+    _lib.call("s4_layernorm_backward", kind, _ptr(dz), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), mean.numel(), D,
+              _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace.numel(), _stream())
+    return dx, dgamma, dbeta
+
+
+def layernorm_channels_backward(dz, x, gamma, eps=1e-5, *, dx=None, dgamma=None, dbeta=None, workspace=None):
+    """Backward of layernorm_channels (s4_layernorm_channels_backward): dz, x
+    [Bt, H, L] float32; returns (dx, dgamma [H], dbeta [H])."""
+    x = _cuda(x, "x", torch.float32)
+    if x.dim() != 3:
+        raise ValueError("x must be [Bt, H, L]")
+    Bt, H, L = x.shape
+    _buffer(_cuda(dz, "dz"), "dz", x.shape, torch.float32, x.device)
+    _buffer(_cuda(gamma, "gamma"), "gamma", (H,), torch.float32, x.device)
+    dx = _buffer(dx, "dx", x.shape, torch.float32, x.device)
+    dgamma = _buffer(dgamma, "dgamma", (H,), torch.float32, x.device)
+    dbeta = _buffer(dbeta, "dbeta", (H,), torch.float32, x.device)
+    workspace = _norm_workspace(H, x.device, workspace)
+    _lib.call("s4_layernorm_channels_backward", _ptr(dz), _ptr(x), _ptr(gamma), float(eps), Bt, H, L, _ptr(dx),
+              _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace.numel(), _stream())
+    return dx, dgamma, dbeta
+
+
+def _tokens(t, name, dtype):
+    """[Bt, T, heads, d] with contiguous heads and evenly spaced tokens (a
+    contiguous tensor, or a slice of a wider projection): its token stride in
+    elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current CUDA device is "
+                         f"cuda:{torch.cuda.current_device()} (use torch.cuda.device({t.device}))")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    Bt, T, H, d = t.shape
+    if Bt * T <= 1:
+        step = max(H * d, 1)
+    elif T > 1:
+        step = t.stride(1)
+    else:
+        step = t.stride(0)
+    even = ((d == 1 or t.stride(3) == 1) and (H == 1 or t.stride(2) == d)
+            and (T <= 1 or Bt == 1 or t.stride(0) == T * step))
+    if t.numel() and not even:
+        raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens")
+    return step if t.numel() else max(H * d, 1)
+
+
+def _delta_args(q, k, v, g, beta):
+    """Shapes and token strides of the gated delta rule's operands."""
+    kind = _dtype(v, "v")
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k [Bt, T, Hk, Dk] and v [Bt, T, Hv, Dv] are wanted")
+    strides = [_tokens(t, n, v.dtype) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    Bt, T, Hk, Dk = q.shape
+    Hv, Dv = v.shape[2:]
+    if tuple(k.shape) != (Bt, T, Hk, Dk) or tuple(v.shape[:2]) != (Bt, T):
+        raise ValueError("shape mismatch between q, k and v")
+    for t, n in ((g, "g"), (beta, "beta")):
+        _buffer(_cuda(t, n), n, (Bt, T, Hv), torch.float32, v.device)
+    return kind, strides, (Bt, T, Hk, Hv, Dk, Dv)
+
+
+def gated_delta_scan(q, k, v, g, beta, state, *, scale=None, out=None):
+    """The gated delta rule token by token (s4_gated_delta_scan): q, k
+    [Bt, T, Hk, Dk], v [Bt, T, Hv, Dv] (float32, bfloat16 or float16), g, beta
+    [Bt, T, Hv] and state [Bt, Hv, Dk, Dv] float32. The state is updated in
+    place; returns o [Bt, T, Hv, Dv]. scale is Dk ** -0.5 by default."""
+    kind, (sq, sk, sv), (Bt, T, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
+    _buffer(_cuda(state, "state"), "state", (Bt, Hv, Dk, Dv), torch.float32, v.device)
+    out = _buffer(out, "out", v.shape, v.dtype, v.device)
+    scale = Dk ** -0.5 if scale is None else scale
+    _lib.call("s4_gated_delta_scan", kind, _ptr(q), sq, _ptr(k), sk, _ptr(v), sv, _ptr(g), _ptr(beta), float(scale),
+              _ptr(state), Bt, T, Hk, Hv, Dk, Dv, _ptr(out), _stream())
+    return out
+
+
+def gated_delta_step(q, k, v, g, beta, state, *, scale=None, out=None):
+    """One token of gated_delta_scan: q, k [Bt, Hk, Dk], v [Bt, Hv, Dv], g,
+    beta [Bt, Hv]; returns o [Bt, Hv, Dv]."""
+    if out is not None:
+        _cuda(out, "out")
+        out = out.unsqueeze(1)
+    return gated_delta_scan(*(t.unsqueeze(1) for t in (q, k, v, g, beta)), state, scale=scale, out=out).squeeze(1)

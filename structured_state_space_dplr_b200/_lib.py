@@ -16,10 +16,13 @@ S4_FLAG_UNSTABLE = 1
 S4_FLAG_NONFINITE = 2
 S4_FLAG_TIMEOUT = 4
 S4_STEP_DENSE, S4_STEP_DIAG, S4_STEP_DPLR = 0, 1, 2
+S4_F32, S4_BF16, S4_F16 = 0, 1, 2
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
+_f = ctypes.c_float
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -61,6 +64,11 @@ SIGNATURES = {
     "s4d_discretize_zoh": (_i, [_p, _p, _p, _i, _i, _p, _p, _p]),
     "s4_recurrent_step": (_i, [_i, _p, _p, _p, _p, _i, _i, _i, _p, _p, _p, _p]),
     "s4_recurrent_scan": (_i, [_i, _p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p]),
+    "s4_layernorm": (_i, [_i, _p, _p, _p, _f, _ll, _i, _p, _p, _p, _p]),
+    "s4_layernorm_backward_workspace_size": (_i, [_i, ctypes.POINTER(_sz)]),
+    "s4_layernorm_backward": (_i, [_i, _p, _p, _p, _p, _p, _ll, _i, _p, _p, _p, _p, _sz, _p]),
+    "s4_layernorm_channels_backward": (_i, [_p, _p, _p, _f, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
+    "s4_gated_delta_scan": (_i, [_i, _p, _ll, _p, _ll, _p, _ll, _p, _p, _f, _p, _i, _i, _i, _i, _i, _i, _p, _p]),
 }
 
 _lib = None

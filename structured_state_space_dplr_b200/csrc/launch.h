@@ -81,6 +81,30 @@ cudaError_t launch_dplr_zoh(const float2 *Lambda, const float2 *P, const float2 
                             const float2 *C, const float *log_dt, int H, int Nh, int L, float2 *Abar,
                             float2 *Bbar, float2 *Cfull, float *K, unsigned *flags, cudaStream_t st);
 
+// ---- norm.cu: layer norm over token rows, and the backward over channels ----
+size_t norm_backward_workspace_bytes(int D);
+cudaError_t launch_layernorm_rows(int dtype, const void *x, const float *gamma, const float *beta, float eps,
+                                  long long rows, int D, void *z, float *mean, float *rstd, cudaStream_t st);
+cudaError_t launch_layernorm_rows_backward(int dtype, const void *dz, const void *x, const float *gamma,
+                                           const float *mean, const float *rstd, long long rows, int D, void *dx,
+                                           float *dgamma, float *dbeta, void *ws, cudaStream_t st);
+cudaError_t launch_layernorm_channels_backward(const float *dz, const float *x, const float *gamma, float eps,
+                                               int Bt, int H, int L, float *dx, float *dgamma, float *dbeta,
+                                               void *ws, cudaStream_t st);
+
+// ---- delta_scan.cu, delta_chunk.cu, delta_grad.cu: the gated delta rule ----
+// n sequences; q, k, v with token strides sq, sk, sv (elements), o contiguous
+struct DeltaArgs {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    void *o;
+    int n, hk, hv, dk, dv;
+    long long sq, sk, sv;
+    float scale;
+};
+// T tokens for each sequence, state [n, hv, dk, dv] in place
+cudaError_t launch_delta_scan(int dtype, const DeltaArgs &a, float *state, int T, cudaStream_t st);
+
 // ---- decode.cu ----
 cudaError_t launch_dplr_discretize(const float2 *Lambda, const float2 *P, const float2 *Q,
                                    const float2 *B, const float2 *C, const float *log_dt, int H, int Nh,

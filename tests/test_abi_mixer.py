@@ -1,0 +1,64 @@
+"""Refusals of the token-major entry points (layer norm, gated delta rule) on
+a machine without a GPU: checked on the host, nothing is launched."""
+import ctypes
+
+import pytest
+
+from structured_state_space_dplr_b200 import _lib
+from structured_state_space_dplr_b200 import build as s4build
+
+FAKE = 0x7f0000000000          # 256-byte aligned, never dereferenced
+FAKE2 = 0x7f1000000000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    s4build.build()
+    return _lib.lib()
+
+
+def p(v):
+    return ctypes.c_void_p(v)
+
+
+def test_norm_entries_reject_bad_arguments(lib):
+    x, ga, be, z, mu, rs, ws = (p(FAKE + 0x1000000 * i) for i in range(7))
+    eps = ctypes.c_float(1e-5)
+    f = lambda dt=0, x=x, ga=ga, eps=eps, rows=8, D=64, z=z, mu=mu: lib.s4_layernorm(  # noqa: E731
+        dt, x, ga, be, eps, rows, D, z, mu, rs, p(0))
+    assert f(dt=3) == f(rows=-1) == f(D=0) == _lib.S4_ERR_INVALID_ARG
+    assert f(D=8193) == f(rows=1 << 31) == _lib.S4_ERR_UNSUPPORTED
+    assert f(x=p(0)) == f(mu=p(0)) == f(eps=ctypes.c_float(0.0)) == f(eps=ctypes.c_float(float("nan"))) == \
+        _lib.S4_ERR_INVALID_ARG
+    assert f(x=p(FAKE + 2)) == _lib.S4_ERR_INVALID_ARG                    # not aligned to a float
+    assert f(z=p(FAKE + 1024)) == f(z=ga) == f(mu=z) == _lib.S4_ERR_INVALID_ARG   # overlaps
+    assert f(rows=0, x=p(0)) == _lib.S4_OK                                 # nothing to do
+    n = ctypes.c_size_t()
+    assert lib.s4_layernorm_backward_workspace_size(64, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.s4_layernorm_backward_workspace_size(8193, ctypes.byref(n)) == _lib.S4_ERR_UNSUPPORTED
+    assert lib.s4_layernorm_backward_workspace_size(0, ctypes.byref(n)) == _lib.S4_ERR_INVALID_ARG
+    lib.s4_layernorm_backward_workspace_size(64, ctypes.byref(n))
+    dz, dx, dg, db = (p(FAKE2 + 0x1000000 * i) for i in range(4))
+    g = lambda dz=dz, dx=dx, dg=dg, ws=ws, nb=n.value, rows=8: lib.s4_layernorm_backward(  # noqa: E731
+        0, dz, x, ga, mu, rs, rows, 64, dx, dg, db, ws, nb, p(0))
+    assert g(dz=p(0)) == g(dg=p(0)) == g(dx=x) == g(dg=db) == _lib.S4_ERR_INVALID_ARG
+    assert g(ws=p(0)) == g(nb=n.value - 1) == g(ws=p(FAKE + 0x6000010)) == _lib.S4_ERR_WORKSPACE
+    c = lambda H=64, L=64, dz=dz, nb=n.value, eps=eps: lib.s4_layernorm_channels_backward(  # noqa: E731
+        dz, x, ga, eps, 2, H, L, dx, dg, db, ws, nb, p(0))
+    assert c(L=100) == c(L=8) == c(L=131072) == _lib.S4_ERR_UNSUPPORTED
+    assert c(H=0) == c(H=8193) == c(dz=p(0)) == c(dz=dx) == c(dz=p(FAKE2 + 8)) == _lib.S4_ERR_INVALID_ARG
+    assert c(nb=16) == _lib.S4_ERR_WORKSPACE
+
+
+def test_gated_delta_scan_rejects_bad_arguments(lib):
+    q, k, v, g, be, st, o = (p(FAKE + 0x1000000 * i) for i in range(7))
+
+    def f(dt=1, q=q, sq=256, sk=256, sv=512, scale=1.0, st=st, Bt=2, T=3, Hk=2, Hv=4, Dk=128, Dv=128, o=o):
+        return lib.s4_gated_delta_scan(dt, q, sq, k, sk, v, sv, g, be, ctypes.c_float(scale), st, Bt, T, Hk, Hv, Dk,
+                                       Dv, o, p(0))
+    bad = _lib.S4_ERR_INVALID_ARG
+    assert f(dt=7) == f(q=p(0)) == f(st=p(0)) == f(Bt=0) == f(T=-1) == f(Hk=0) == f(Hv=3) == f(Dk=0) == bad
+    assert f(Dk=100) == f(Dv=136) == f(Dv=4) == _lib.S4_ERR_UNSUPPORTED
+    assert f(sq=255) == f(sq=248) == f(sv=504) == f(sk=260) == f(scale=float("inf")) == bad
+    assert f(q=p(FAKE + 8)) == f(o=v) == f(st=o) == f(o=q) == bad
+    assert f(T=0, q=p(0)) == _lib.S4_OK

@@ -641,6 +641,41 @@ s4_status s4_gated_delta_scan(s4_dtype dtype, const void *q, long long q_stride,
                               float *state, int Bt, int T, int Hk, int Hv, int Dk, int Dv, void *o,
                               cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * s4_gated_delta_forward -- the gated delta rule over whole sequences in
+ * chunks of 64 tokens: inside a chunk dense products on the tensor cores,
+ * from chunk to chunk the recurrence of the states. Operands as for
+ * s4_gated_delta_scan; `tokens` counts the tokens of all Bt sequences:
+ *   cu_seqlens NULL: Bt sequences of tokens / Bt each, q [Bt, T, Hk, Dk] ...
+ *   cu_seqlens [Bt + 1] int, device: the sequences lie one after the other in
+ *     q [1, tokens, Hk, Dk] ..., sequence i in [cu[i], cu[i+1]); empty ones
+ *     are fine, and rows of o outside all of them are left as they were.
+ *     Offsets have to rise from >= 0 to <= tokens; others are clamped (the
+ *     results are then meaningless, no access is out of range).
+ *   initial_state (NULL: zeros), final_state (NULL: not wanted): [Bt, Hv, Dk,
+ *     Dv] float; they may be the same array. An empty sequence's final state
+ *     is its initial state.
+ *   keep != 0 leaves in the workspace what s4_gated_delta_backward reads
+ *     (states before the chunks and the chunks' writes).
+ *   workspace: s4_gated_delta_workspace_size(Bt, tokens, Hv, Dk, Dv, keep)
+ *     bytes, device, 256-byte aligned, caller-owned.
+ *   d_flags (nullable): S4_FLAG_TIMEOUT if a bounded wait ran out.
+ * Operands that are not bf16 are split into bf16 parts (three for float: 24
+ * bits) and accumulated in float: results are as good as float arithmetic's.
+ * Errors: as s4_gated_delta_scan; tokens < 0 or not a multiple of Bt (without
+ * cu_seqlens) -> S4_ERR_INVALID_ARG; tokens >= 2^31, or (tokens / 64 + Bt) Hv
+ * >= 2^31 -> S4_ERR_UNSUPPORTED; workspace too small or misaligned ->
+ * S4_ERR_WORKSPACE.
+ * ------------------------------------------------------------------------ */
+s4_status s4_gated_delta_workspace_size(int Bt, long long tokens, int Hv, int Dk, int Dv, int keep, size_t *bytes);
+
+s4_status s4_gated_delta_forward(s4_dtype dtype, const void *q, long long q_stride, const void *k,
+                                 long long k_stride, const void *v, long long v_stride, const float *g,
+                                 const float *beta, float scale, const float *initial_state,
+                                 const int *cu_seqlens, int Bt, long long tokens, int Hk, int Hv, int Dk, int Dv,
+                                 void *o, float *final_state, int keep, void *workspace, size_t workspace_bytes,
+                                 unsigned *d_flags, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

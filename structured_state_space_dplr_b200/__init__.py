@@ -28,7 +28,7 @@ __all__ = [
     "fft_conv_host", "fft_conv_apply_adjoint", "fft_conv_kernel_grad", "fft_conv_kernel_grad_workspace_size",
     "kernel_dplr_backward", "kernel_dplr_backward_workspace_size", "s4d_kernel_vandermonde_backward", "load",
     "layernorm", "layernorm_backward", "layernorm_backward_workspace_size", "layernorm_channels_backward",
-    "gated_delta_step", "gated_delta_scan",
+    "gated_delta_step", "gated_delta_scan", "gated_delta_workspace_size", "gated_delta_forward",
 ]
 
 
@@ -743,3 +743,47 @@ def gated_delta_step(q, k, v, g, beta, state, *, scale=None, out=None):
         _cuda(out, "out")
         out = out.unsqueeze(1)
     return gated_delta_scan(*(t.unsqueeze(1) for t in (q, k, v, g, beta)), state, scale=scale, out=out).squeeze(1)
+
+
+def gated_delta_workspace_size(Bt, tokens, Hv, Dk, Dv, keep=False) -> int:
+    """Bytes of workspace gated_delta_forward needs for `tokens` tokens in all
+    of Bt sequences (keep: and for gated_delta_backward after it)."""
+    n = ctypes.c_size_t(0)
+    _lib.call("s4_gated_delta_workspace_size", int(Bt), int(tokens), int(Hv), int(Dk), int(Dv), int(bool(keep)),
+              ctypes.byref(n))
+    return n.value
+
+
+def _sequences(cu_seqlens, Bt):
+    if cu_seqlens is None:
+        return Bt
+    _cuda(cu_seqlens, "cu_seqlens", torch.int32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or Bt != 1:
+        raise ValueError("cu_seqlens is [N + 1] for N >= 1 sequences packed in [1, T, ...]")
+    return cu_seqlens.numel() - 1
+
+
+def gated_delta_forward(q, k, v, g, beta, *, scale=None, initial_state=None, cu_seqlens=None, keep=False, out=None,
+                        final_state=None, workspace=None, flags=None):
+    """The gated delta rule over whole sequences, in chunks
+    (s4_gated_delta_forward): q, k [Bt, T, Hk, Dk], v [Bt, T, Hv, Dv]
+    (float32, bfloat16 or float16), g, beta [Bt, T, Hv] float32; with
+    cu_seqlens (int32, [N + 1]) N sequences packed in [1, T, ...].
+    initial_state [N, Hv, Dk, Dv] float32 (zeros by default; final_state may be
+    the same tensor). Returns (o, final_state, workspace); with keep the
+    workspace holds what gated_delta_backward needs."""
+    kind, (sq, sk, sv), (Bt, T, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
+    n, dev = _sequences(cu_seqlens, Bt), v.device
+    if initial_state is not None:
+        _buffer(_cuda(initial_state, "initial_state"), "initial_state", (n, Hv, Dk, Dv), torch.float32, dev)
+    out = _buffer(out, "out", v.shape, v.dtype, dev)
+    final_state = _buffer(final_state, "final_state", (n, Hv, Dk, Dv), torch.float32, dev)
+    if workspace is None:
+        need = gated_delta_workspace_size(n, Bt * T, Hv, Dk, Dv, keep)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _cuda(workspace, "workspace", torch.uint8)
+    scale = Dk ** -0.5 if scale is None else scale
+    _lib.call("s4_gated_delta_forward", kind, _ptr(q), sq, _ptr(k), sk, _ptr(v), sv, _ptr(g), _ptr(beta),
+              float(scale), _ptr(initial_state), _ptr(cu_seqlens), n, Bt * T, Hk, Hv, Dk, Dv, _ptr(out),
+              _ptr(final_state), int(bool(keep)), _ptr(workspace), workspace.numel(), _flags_ptr(flags), _stream())
+    return out, final_state, workspace

@@ -75,6 +75,32 @@ double span(int dtype, double tokens, long long stride, long long row) {
     return tokens < 1 ? 0.0 : ((tokens - 1) * (double)stride + (double)row) * (double)dtype_size(dtype);
 }
 
+// the workspace of the chunked form: units of T and PT and factors, then (keep)
+// the states before the chunks, E, the states' gradients behind the chunks and dR
+struct DeltaWork {
+    double units;
+    size_t state, rows, prep, total;   // bytes of one kind
+};
+DeltaWork delta_work(int Bt, long long tokens, int Hv, int Dk, int Dv, int keep) {
+    DeltaWork w;
+    const long long units = (tokens / 64 + Bt) * (long long)Hv;
+    w.units = (double)(tokens / 64 + Bt) * Hv;
+    w.prep = (size_t)units * s4::delta_unit_bytes();
+    w.state = keep ? (size_t)units * Dk * Dv * 4 : 0;
+    w.rows = keep ? (size_t)units * 64 * Dv * 4 : 0;
+    w.total = w.prep + 2 * w.state + 2 * w.rows;
+    return w;
+}
+
+// sizes of the chunked form; `tokens` in all, packed (cu) or Bt times the same number
+s4_status chunk_sizes(int dtype, bool packed, int Bt, long long tokens, int Hk, int Hv, int Dk, int Dv) {
+    s4_status s = delta_sizes(dtype, Bt, Hk, Hv, Dk, Dv);
+    if (s != S4_OK) return s;
+    if (tokens < 0 || (!packed && tokens % Bt)) return S4_ERR_INVALID_ARG;
+    if (tokens > 0x7fffffffLL || delta_work(Bt, tokens, Hv, Dk, Dv, 0).units > 2147483647.0) return S4_ERR_UNSUPPORTED;
+    return S4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -163,8 +189,56 @@ s4_status s4_gated_delta_scan(s4_dtype dtype, const void *q, long long q_stride,
                      {state, 4.0 * Bt * Hv * Dk * Dv, true},
                      {o, span(dtype, tok, (long long)Hv * Dv, (long long)Hv * Dv), true}}))
         return S4_ERR_INVALID_ARG;
-    s4::DeltaArgs a{q, k, v, g, beta, o, Bt, Hk, Hv, Dk, Dv, q_stride, k_stride, v_stride, scale};
+    s4::DeltaArgs a{q, k, v, g, beta, o, Bt, Hk, Hv, Dk, Dv, q_stride, k_stride, v_stride, scale, nullptr, T, Bt * (long long)T};
     return cuda_status(s4::launch_delta_scan(dtype, a, state, T, stream));
+}
+
+s4_status s4_gated_delta_workspace_size(int Bt, long long tokens, int Hv, int Dk, int Dv, int keep, size_t *bytes) {
+    if (!bytes) return S4_ERR_INVALID_ARG;
+    s4_status s = chunk_sizes(S4_F32, true, Bt, tokens, 1, Hv, Dk, Dv);
+    if (s != S4_OK) return s;
+    *bytes = delta_work(Bt, tokens, Hv, Dk, Dv, keep).total;
+    return S4_OK;
+}
+
+s4_status s4_gated_delta_forward(s4_dtype dtype, const void *q, long long q_stride, const void *k, long long k_stride,
+                                 const void *v, long long v_stride, const float *g, const float *beta, float scale,
+                                 const float *initial_state, const int *cu_seqlens, int Bt, long long tokens, int Hk,
+                                 int Hv, int Dk, int Dv, void *o, float *final_state, int keep, void *workspace,
+                                 size_t workspace_bytes, unsigned *d_flags, cudaStream_t stream) {
+    s4_status s = chunk_sizes(dtype, cu_seqlens != nullptr, Bt, tokens, Hk, Hv, Dk, Dv);
+    if (s != S4_OK) return s;
+    if (!std::isfinite(scale) || !strides_ok(dtype, Hk, Hv, Dk, Dv, q_stride, k_stride, v_stride))
+        return S4_ERR_INVALID_ARG;
+    if (tokens > 0 && any_null({q, k, v, g, beta, o})) return S4_ERR_INVALID_ARG;
+    if (!aligned(16, {q, k, v, o, initial_state, final_state}) || !aligned(4, {g, beta, cu_seqlens, d_flags}))
+        return S4_ERR_INVALID_ARG;
+    const DeltaWork w = delta_work(Bt, tokens, Hv, Dk, Dv, keep);
+    if (!workspace || !aligned(256, {workspace}) || workspace_bytes < w.total) return S4_ERR_WORKSPACE;
+    const double tok = (double)tokens, gate = tok * Hv * 4.0, st = 4.0 * Bt * Hv * Dk * Dv;
+    // final_state may be initial_state: a state is read before it is written
+    if (overlapping({{q, span(dtype, tok, q_stride, (long long)Hk * Dk), false},
+                     {k, span(dtype, tok, k_stride, (long long)Hk * Dk), false},
+                     {v, span(dtype, tok, v_stride, (long long)Hv * Dv), false},
+                     {g, gate, false},
+                     {beta, gate, false},
+                     {cu_seqlens, 4.0 * (Bt + 1.0), false},
+                     {initial_state == final_state ? nullptr : initial_state, st, false},
+                     {o, span(dtype, tok, (long long)Hv * Dv, (long long)Hv * Dv), true},
+                     {final_state, st, true},
+                     {d_flags, 4.0, true},
+                     {workspace, (double)workspace_bytes, true}}))
+        return S4_ERR_INVALID_ARG;
+    s4::DeltaArgs a{q,  k,  v,        g,        beta,     o,     Bt,         Hk,                        Hv,    Dk,
+                    Dv, q_stride, k_stride, v_stride, scale, cu_seqlens, cu_seqlens ? 0 : (int)(tokens / Bt), tokens};
+    char *p = (char *)workspace;
+    float *ks = keep ? (float *)(p + w.prep) : nullptr, *ke = keep ? (float *)(p + w.prep + w.state) : nullptr;
+    if (tokens > 0) {
+        s = cuda_status(s4::launch_delta_prep(dtype, a, workspace, d_flags, stream));
+        if (s != S4_OK) return s;
+    }
+    return cuda_status(
+        s4::launch_delta_forward(dtype, a, initial_state, final_state, workspace, ks, ke, d_flags, stream));
 }
 
 }  // extern "C"

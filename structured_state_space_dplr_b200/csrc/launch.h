@@ -101,9 +101,21 @@ struct DeltaArgs {
     int n, hk, hv, dk, dv;
     long long sq, sk, sv;
     float scale;
+    // the chunked form: n sequences of t tokens each, or between the offsets cu [n + 1]; tokens in all
+    const int *cu;
+    int t;
+    long long tokens;
 };
 // T tokens for each sequence, state [n, hv, dk, dv] in place
 cudaError_t launch_delta_scan(int dtype, const DeltaArgs &a, float *state, int T, cudaStream_t st);
+
+// bytes of the images and factors of one chunk and value head
+size_t delta_unit_bytes();
+// the chunks' images of T and PT and the gates' factors
+cudaError_t launch_delta_prep(int dtype, const DeltaArgs &a, void *ws, unsigned *flags, cudaStream_t st);
+// o and the last states; keep_s, keep_e (or null): the state before every chunk and E of every chunk
+cudaError_t launch_delta_forward(int dtype, const DeltaArgs &a, const float *init, float *last, const void *ws,
+                                 float *keep_s, float *keep_e, unsigned *flags, cudaStream_t st);
 
 // ---- decode.cu ----
 cudaError_t launch_dplr_discretize(const float2 *Lambda, const float2 *P, const float2 *Q,

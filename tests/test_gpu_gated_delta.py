@@ -1,0 +1,71 @@
+"""The chunked gated delta rule (forward, backward) against the fp64 oracle."""
+import numpy as np
+import pytest
+
+from gpu_helpers import torch_cuda
+from oracle import delta
+from test_gpu_gated_delta_scan import f64, make
+
+pytestmark = pytest.mark.gpu
+
+NAMES = ("q", "k", "v", "g", "beta")
+
+# Every product is a float sum of 24-bit operands: its error is a few 2^-24 of
+# the sum of its terms' sizes. A chunk passes five products one after the
+# other (T's two, K S, T R, K^T E) of up to 128 terms of 3 parts each, the
+# tensor cores add groups of 16 terms with a truncated carry (one step of the
+# largest, 2^-23, a group: 24 groups), and T is solved in float over 64 rows.
+# Errors of the state are damped like the state. Relative 2-norm over a
+# tensor: 5 products * 24 groups * 2^-23 = 1.5e-5 if every group erred fully
+# and the same way; the signs differ, so that a root of the count remains:
+# 5 * sqrt(24) * 2^-23 = 3e-6, and half as much again for T.
+REL = 4.5e-6
+
+
+def check(got, ref, dtype, what, terms=None):
+    torch = torch_cuda()
+    step = torch.finfo(dtype).eps / 2 if dtype != torch.float32 else 0.0
+    real = ~np.isnan(ref)
+    g, r = f64(got)[real], ref[real]
+    assert np.isfinite(g).all(), f"{what}: not finite"
+    if not r.size:
+        return
+    norm = np.linalg.norm(r)
+    err = np.linalg.norm(g - r)
+    # the norm of the roundings to 16 bits is at most a half step of each value
+    assert err <= (REL + step) * norm + 1e-30, f"{what}: {err / norm}"
+    rms = norm / np.sqrt(r.size)
+    big = (np.abs(g - r) / np.maximum(np.abs(r), rms)).max()
+    assert big <= 1.01 * step + 16 * REL, f"{what}: one value {big}"
+
+
+def forward(d, **more):
+    import structured_state_space_dplr_b200 as s4
+    torch = torch_cuda()
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = s4.gated_delta_forward(*(d[n] for n in NAMES), flags=flags, **more)
+    assert flags.item() == 0
+    return r
+
+
+SHAPES = [(1, 64, 1, 1, 64, 64), (1, 1, 1, 1, 8, 8), (2, 65, 1, 2, 64, 64), (1, 130, 2, 2, 128, 128),
+          (2, 63, 2, 6, 96, 80), (3, 200, 1, 3, 72, 128), (1, 321, 2, 4, 128, 40), (5, 7, 4, 4, 16, 120),
+          (2, 128, 3, 3, 40, 8)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+def test_forward(shape, dtype):
+    torch = torch_cuda()
+    d = make(*shape, dtype=dtype)
+    Dk = shape[4]
+    args = [f64(d[n]) for n in NAMES]
+    ref, last = delta.gated_delta(*args, Dk ** -0.5)
+    o, got, _ = forward(d)
+    check(o, ref, d["v"].dtype, "o")
+    check(got, last, torch.float32, "state")
+    ref, last = delta.gated_delta(*args, 0.7, f64(d["state"]))
+    for keep in (False, True):
+        o, got, _ = forward(d, scale=0.7, initial_state=d["state"], keep=keep)
+        check(o, ref, d["v"].dtype, "o from a state")
+        check(got, last, torch.float32, "state from a state")

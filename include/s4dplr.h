@@ -657,8 +657,8 @@ s4_status s4_gated_delta_scan(s4_dtype dtype, const void *q, long long q_stride,
  *     is its initial state.
  *   keep != 0 leaves in the workspace what s4_gated_delta_backward reads
  *     (states before the chunks and the chunks' writes).
- *   workspace: s4_gated_delta_workspace_size(Bt, tokens, Hv, Dk, Dv, keep)
- *     bytes, device, 256-byte aligned, caller-owned.
+ *   workspace: s4_gated_delta_workspace_size(...) bytes for the
+ *     same sizes, device, 256-byte aligned, caller-owned.
  *   d_flags (nullable): S4_FLAG_TIMEOUT if a bounded wait ran out.
  * Operands that are not bf16 are split into bf16 parts (three for float: 24
  * bits) and accumulated in float: results are as good as float arithmetic's.
@@ -667,7 +667,8 @@ s4_status s4_gated_delta_scan(s4_dtype dtype, const void *q, long long q_stride,
  * >= 2^31 -> S4_ERR_UNSUPPORTED; workspace too small or misaligned ->
  * S4_ERR_WORKSPACE.
  * ------------------------------------------------------------------------ */
-s4_status s4_gated_delta_workspace_size(int Bt, long long tokens, int Hv, int Dk, int Dv, int keep, size_t *bytes);
+s4_status s4_gated_delta_workspace_size(s4_dtype dtype, int Bt, long long tokens, int Hk, int Hv, int Dk, int Dv,
+                                        int keep, size_t *bytes);
 
 s4_status s4_gated_delta_forward(s4_dtype dtype, const void *q, long long q_stride, const void *k,
                                  long long k_stride, const void *v, long long v_stride, const float *g,

@@ -745,12 +745,15 @@ def gated_delta_step(q, k, v, g, beta, state, *, scale=None, out=None):
     return gated_delta_scan(*(t.unsqueeze(1) for t in (q, k, v, g, beta)), state, scale=scale, out=out).squeeze(1)
 
 
-def gated_delta_workspace_size(Bt, tokens, Hv, Dk, Dv, keep=False) -> int:
+def gated_delta_workspace_size(dtype, Bt, tokens, Hk, Hv, Dk, Dv, keep=False) -> int:
     """Bytes of workspace gated_delta_forward needs for `tokens` tokens in all
-    of Bt sequences (keep: and for gated_delta_backward after it)."""
+    of Bt sequences of the torch dtype (keep: and for gated_delta_backward
+    after it)."""
+    if dtype not in _DTYPES:
+        raise TypeError("float32, bfloat16 or float16 is wanted")
     n = ctypes.c_size_t(0)
-    _lib.call("s4_gated_delta_workspace_size", int(Bt), int(tokens), int(Hv), int(Dk), int(Dv), int(bool(keep)),
-              ctypes.byref(n))
+    _lib.call("s4_gated_delta_workspace_size", _DTYPES[dtype], int(Bt), int(tokens), int(Hk), int(Hv), int(Dk),
+              int(Dv), int(bool(keep)), ctypes.byref(n))
     return n.value
 
 
@@ -779,7 +782,7 @@ def gated_delta_forward(q, k, v, g, beta, *, scale=None, initial_state=None, cu_
     out = _buffer(out, "out", v.shape, v.dtype, dev)
     final_state = _buffer(final_state, "final_state", (n, Hv, Dk, Dv), torch.float32, dev)
     if workspace is None:
-        need = gated_delta_workspace_size(n, Bt * T, Hv, Dk, Dv, keep)
+        need = gated_delta_workspace_size(v.dtype, n, Bt * T, Hk, Hv, Dk, Dv, keep)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _cuda(workspace, "workspace", torch.uint8)
     scale = Dk ** -0.5 if scale is None else scale

@@ -78,14 +78,12 @@ double span(int dtype, double tokens, long long stride, long long row) {
 // the workspace of the chunked form: units of T and PT and factors, then (keep)
 // the states before the chunks, E, the states' gradients behind the chunks and dR
 struct DeltaWork {
-    double units;
     size_t state, rows, prep, total;   // bytes of one kind
 };
-DeltaWork delta_work(int Bt, long long tokens, int Hv, int Dk, int Dv, int keep) {
+DeltaWork delta_work(int dtype, int Bt, long long tokens, int Hk, int Hv, int Dk, int Dv, int keep) {
     DeltaWork w;
     const long long units = (tokens / 64 + Bt) * (long long)Hv;
-    w.units = (double)(tokens / 64 + Bt) * Hv;
-    w.prep = (size_t)units * s4::delta_unit_bytes();
+    w.prep = s4::delta_prep_bytes(dtype, tokens, Bt, Hk, Hv, Dk);
     w.state = keep ? (size_t)units * Dk * Dv * 4 : 0;
     w.rows = keep ? (size_t)units * 64 * Dv * 4 : 0;
     w.total = w.prep + 2 * w.state + 2 * w.rows;
@@ -97,7 +95,7 @@ s4_status chunk_sizes(int dtype, bool packed, int Bt, long long tokens, int Hk, 
     s4_status s = delta_sizes(dtype, Bt, Hk, Hv, Dk, Dv);
     if (s != S4_OK) return s;
     if (tokens < 0 || (!packed && tokens % Bt)) return S4_ERR_INVALID_ARG;
-    if (tokens > 0x7fffffffLL || delta_work(Bt, tokens, Hv, Dk, Dv, 0).units > 2147483647.0) return S4_ERR_UNSUPPORTED;
+    if (tokens > 0x7fffffffLL || (double)(tokens / 64 + Bt) * Hv > 2147483647.0) return S4_ERR_UNSUPPORTED;
     return S4_OK;
 }
 
@@ -193,11 +191,12 @@ s4_status s4_gated_delta_scan(s4_dtype dtype, const void *q, long long q_stride,
     return cuda_status(s4::launch_delta_scan(dtype, a, state, T, stream));
 }
 
-s4_status s4_gated_delta_workspace_size(int Bt, long long tokens, int Hv, int Dk, int Dv, int keep, size_t *bytes) {
+s4_status s4_gated_delta_workspace_size(s4_dtype dtype, int Bt, long long tokens, int Hk, int Hv, int Dk, int Dv,
+                                        int keep, size_t *bytes) {
     if (!bytes) return S4_ERR_INVALID_ARG;
-    s4_status s = chunk_sizes(S4_F32, true, Bt, tokens, 1, Hv, Dk, Dv);
+    s4_status s = chunk_sizes(dtype, true, Bt, tokens, Hk, Hv, Dk, Dv);
     if (s != S4_OK) return s;
-    *bytes = delta_work(Bt, tokens, Hv, Dk, Dv, keep).total;
+    *bytes = delta_work(dtype, Bt, tokens, Hk, Hv, Dk, Dv, keep).total;
     return S4_OK;
 }
 
@@ -213,7 +212,7 @@ s4_status s4_gated_delta_forward(s4_dtype dtype, const void *q, long long q_stri
     if (tokens > 0 && any_null({q, k, v, g, beta, o})) return S4_ERR_INVALID_ARG;
     if (!aligned(16, {q, k, v, o, initial_state, final_state}) || !aligned(4, {g, beta, cu_seqlens, d_flags}))
         return S4_ERR_INVALID_ARG;
-    const DeltaWork w = delta_work(Bt, tokens, Hv, Dk, Dv, keep);
+    const DeltaWork w = delta_work(dtype, Bt, tokens, Hk, Hv, Dk, Dv, keep);
     if (!workspace || !aligned(256, {workspace}) || workspace_bytes < w.total) return S4_ERR_WORKSPACE;
     const double tok = (double)tokens, gate = tok * Hv * 4.0, st = 4.0 * Bt * Hv * Dk * Dv;
     // final_state may be initial_state: a state is read before it is written

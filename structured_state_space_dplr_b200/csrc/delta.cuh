@@ -32,8 +32,14 @@ namespace s4 {
 namespace delta {
 
 constexpr int kC = 64;                         // tokens of a chunk
-constexpr int kTpImage = 2 * kC * kC * 2;      // 16 KB: one part of [T; PT], 128 rows x 64 columns
+// One part of T and PT in the workspace. Both are lower triangular: the 16
+// columns of step ks have rows 16 ks and up only, two column groups of 64 - 16
+// ks rows of T and then as many of PT.
+constexpr int kTpImage = 10240;
 constexpr int kTpBytes = 3 * kTpImage;
+__host__ __device__ constexpr int tp_offset(int ks) { return 4096 * ks - 512 * ks * (ks - 1); }
+__host__ __device__ constexpr int tp_rows(int ks) { return (kC - 16 * ks) * 16; }      // bytes: T's rows of a group
+__host__ __device__ constexpr int tp_group(int ks) { return 2 * tp_rows(ks); }         // bytes of a column group
 constexpr int kFacBytes = 2 * kC * 4;          // e^G and beta e^(G_C - G)
 constexpr int kUnitBytes = kTpBytes + kFacBytes;   // workspace of one chunk and value head
 constexpr uint32_t kSpinLimit = 1u << 22;
@@ -75,6 +81,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// two floats at once
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_get(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // a and b as N bf16 parts each, a in the low halves; each part is what the
 // ones before it leave, rounded to nearest
 template <int N>
@@ -82,8 +102,7 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&p)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         p[i] = pack2(a, b);
-        a -= lo_f(p[i]);
-        b -= hi_f(p[i]);
+        if (i + 1 < N) f2_get(f2_sub(f2(a, b), f2(lo_f(p[i]), hi_f(p[i]))), a, b);
     }
 }
 
@@ -158,8 +177,10 @@ __device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t (&v)[8]) {
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 16 floats (consecutive K elements of a lane) as three parts of 8 columns each
-__device__ __forceinline__ void tm_split16(uint32_t hi, uint32_t mid, uint32_t lo, const float (&v)[16]) {
+// 16 floats (consecutive K elements of a lane, one K step) as three parts of
+// 8 columns: the high and middle ones side by side at `at`, which is where an
+// accumulator of the same 16 columns lies, the low one at `lo`
+__device__ __forceinline__ void tm_split16(uint32_t at, uint32_t lo, const float (&v)[16]) {
     uint32_t p[3][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -169,16 +190,61 @@ __device__ __forceinline__ void tm_split16(uint32_t hi, uint32_t mid, uint32_t l
         p[1][i] = s[1];
         p[2][i] = s[2];
     }
-    tm_st8(hi, p[0]);
-    tm_st8(mid, p[1]);
+    tm_st8(at, p[0]);
+    tm_st8(at + 8, p[1]);
     tm_st8(lo, p[2]);
+}
+
+// 16 bytes to shared memory, zeros where `in` is false
+__device__ __forceinline__ void cp16(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(saddr(dst)), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
+
+// `rows` rows (zeros up to 64) of dk elements (zeros up to DKT) into the parts'
+// images, `part` bytes apart, column groups `group` bytes apart, from row 0 of
+// dst. Warp w of nw takes every nw-th group of 8 rows, 4 column groups at a
+// time. bf16 goes asynchronously (umma::cp_async_wait_all), the others by
+// registers.
+template <typename T, int DKT>
+__device__ __forceinline__ void load_image(unsigned char *dst, int part, int group, const T *src, long long stride,
+                                           int rows, int dk, int w, int nw) {
+    constexpr int NB = Parts<T>::n;
+    const int r = threadIdx.x & 7, cl = (threadIdx.x & 31) >> 3;
+    src += r * stride + 8 * cl;
+    dst += r * 16 + cl * group;
+    for (int rg = w; rg < kC / 8; rg += nw) {
+        const T *p = src + 8 * rg * stride;
+        unsigned char *d = dst + rg * 128;
+        const bool row = 8 * rg + r < rows;
+        if constexpr (NB == 1) {
+#pragma unroll
+            for (int n = 0; n < DKT / 32; ++n) {
+                const bool in = row && 8 * cl + 32 * n < dk;
+                cp16(d + 4 * n * group, in ? p + 32 * n : src, in);
+            }
+        } else {
+            uint4 v[DKT / 32][NB];
+#pragma unroll
+            for (int n = 0; n < DKT / 32; ++n) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) v[n][i] = make_uint4(0, 0, 0, 0);
+                if (row && 8 * cl + 32 * n < dk) load_parts(p + 32 * n, v[n]);
+            }
+#pragma unroll
+            for (int n = 0; n < DKT / 32; ++n)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) *reinterpret_cast<uint4 *>(d + i * part + 4 * n * group) = v[n][i];
+        }
+    }
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *m) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(m)) : "memory");
 }
+// bytes that copies will bring in the current phase; the caller has not arrived yet
 __device__ __forceinline__ void mbar_expect(uint64_t *m, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(m)), "r"(bytes) : "memory");
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(saddr(m)), "r"(bytes) : "memory");
 }
 // bytes a multiple of 16, both addresses 16-byte aligned
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *m) {
@@ -187,6 +253,51 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  "l"(src), "r"(bytes), "r"(saddr(m))
                  : "memory");
 }
+
+__device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+// shared memory (written with a fence.proxy.async behind) to global memory; by one thread
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(saddr(src)), "r"(bytes)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// the thread's stores have read their source / are done
+__device__ __forceinline__ void bulk_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// `rows` rows of dv elements (zeros up to 64 rows) to consecutive places of
+// dst, by thread t of nt; done when m has this thread's arrival (one of those
+// it was initialised with). (Bulk copies of single rows take ~70 cycles each
+// to issue, four times as long in all.)
+template <typename T>
+__device__ __forceinline__ void load_rows(unsigned char *dst, const T *src, long long stride, int rows, int dv, int t,
+                                          int nt, uint64_t *m) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const int per = dv / E, step = nt / per, r0 = t / per, c = t - r0 * per;   // per <= 32 <= nt
+    if (r0 < step) {
+        const T *p = src + r0 * stride + c * E;
+        for (int r = r0; r < kC; r += step, p += step * stride) cp16(dst + (r * per + c) * 16, r < rows ? p : src, r < rows);
+    }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(saddr(m)) : "memory");
+}
+
+// one lane of a converged warp; with warp-uniform operands the tensor-core
+// instructions behind it issue back to back (a product of N columns every N / 2
+// cycles; behind a test of the lane number they took up to 280)
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+template <typename V>
+__device__ __forceinline__ V uniform(V v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// the workspace: units of (slot, value head), then the images of [K; Q] of (slot, key head)
+template <typename T, int DKT>
+__host__ __device__ constexpr int kq_bytes() { return Parts<T>::n * 2 * kC * DKT * 2; }
 
 }  // namespace delta
 }  // namespace s4

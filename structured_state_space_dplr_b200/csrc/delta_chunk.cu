@@ -4,18 +4,19 @@
 // Everything is kept transposed, value channel = tensor-memory lane, so that
 // the three products of a chunk that depend on each other take their left
 // operand from tensor memory, written there by the threads that computed it,
-// and their right operand from the natural image of K, Q or [T; PT]:
-//     D1 = S0^T [K; Q]^T          (128 x 64 each)
-//     R^T = V^T - e^G D1k  ->  D2 = R^T [T; PT]^T  = [E^T | (PT R)^T]
-//     (beta e^(G_C - G) E)^T  ->  D3 = (..)^T K     (128 x Dk)
-//     S1^T = e^(G_C) S0^T + D3,   O^T = scale e^G D1q + D2o.
+// and their right operand from the natural image of [K; Q] or [T; PT]:
+//     D1 = S0^T [K; Q]^T                           (128 x 128)
+//     R^T = V^T - e^G D1k,   D2 = R^T [T; PT]^T    (E^T and (PT R)^T)
+//     D3 = (beta e^(G_C - G) E)^T K                (128 x Dk)
+//     S1^T = e^(G_C) S0^T + D3,   O^T = scale e^G D1q + (PT R)^T.
 // Roles: warps 0-7 the element-wise steps (two warps per lane quarter, each
 // half the columns), warp 8 issues the products, warps 9-11 load.
 //
-// What bounds it: the chain of a chunk, three products and three passes of
-// splitting and tensor-memory traffic, one after the other; the products that
-// are not in the chain (D1q, D2o) and the output run beside it. A block needs
-// all 512 tensor-memory columns, so there is one per SM.
+// What bounds it: the chain of a chunk, three products and three element-wise
+// passes one after the other, most of it the splitting in the passes. A
+// product starts with the first 16 columns of its operand; Q's and PT's
+// products and the output run in the chain's gaps. A block needs all 512
+// tensor-memory columns, so there is one per SM.
 #include "delta.cuh"
 #include "s4dplr.h"
 
@@ -26,47 +27,95 @@ using namespace delta;
 
 constexpr int kEpiWarps = 8, kLoadWarps = 3, kThreads = (kEpiWarps + 1 + kLoadWarps) * 32;
 
-// tensor-memory columns: the state's parts (and D3 in their place), the parts
-// of R (in the place of D1k) and of beta e^(G_C - G) E (in the place of D2e),
-// D1q, D2o. A warp overwrites only columns that it alone has read: half h of
-// the K range holds its high and middle parts in the accumulator columns of
-// the same half.
-constexpr int kTmS = 0, kTmR = 192, kTmE = 288, kTmQ = 384, kTmO = 448;
+// Tensor-memory columns. An operand's high and middle parts take the place of
+// the accumulator it was computed from, 16 columns by 16 columns, so a warp
+// overwrites only what it alone has read:
+//   kTmS   the state's parts, D3 in their place (128), low parts at kTmSl
+//   kTmK   S0^T K^T (64), then R's parts, low ones at kTmRl
+//   kTmE   E^T (64), then the parts of beta e^(G_C - G) E, low ones at kTmEl
+//   kTmQ, kTmO   S0^T Q^T and (PT R)^T (64 each)
+constexpr int kTmS = 0, kTmSl = 128, kTmK = 192, kTmE = 256, kTmQ = 320, kTmO = 384, kTmRl = 448, kTmEl = 480;
 
-// column of part p, K step ks (8 columns of 16 elements), in an operand of K
-// elements that lies in the place of an accumulator of K columns
-template <int K>
-__device__ __forceinline__ uint32_t part_col(int p, int ks) {
-    constexpr int half = K / 2;
-    const int h = ks / (half / 16), r = ks % (half / 16);
-    return p < 2 ? h * half + p * (half / 2) + 8 * r : K + h * (half / 2) + 8 * r;
+// parts of [K; Q], 128 rows; then T and PT and factors, V as it is
+template <typename T, int DKT>
+struct Stage {
+    static constexpr int NB = Parts<T>::n;
+    static constexpr int kImg = 2 * kC * DKT * 2, kTp = NB * kImg, kV = kTp + kUnitBytes;
+    static __host__ __device__ int bytes(int dv) { return kV + kC * dv * (int)sizeof(T); }
+    static __host__ __device__ int count(int dv) { return 2 * bytes(dv) + 256 <= 232448 ? 2 : 1; }
+};
+
+enum { bFull = 0, bEmpty = 2, bS = 4, bR = 8, bE = 10, bO = 12, bM1, bM2, bMq, bM2o, bM3, bCount };
+
+// 16 consecutive floats of shared memory (16-byte aligned, the same for the warp)
+__device__ __forceinline__ void get16(const float *p, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 f = reinterpret_cast<const float4 *>(p)[i];
+        v[4 * i] = f.x;
+        v[4 * i + 1] = f.y;
+        v[4 * i + 2] = f.z;
+        v[4 * i + 3] = f.w;
+    }
+}
+
+// 16 tokens of this lane's channel to o, `row` elements apart, the first n of
+// them. 16-bit types: neighbouring lanes swap so that each stores two channels
+// of every other token in one word (dv is even: both channels are there or not).
+template <typename T>
+__device__ __forceinline__ void store16(T *o, long long row, const float (&x)[16], int lane, bool vin, int n) {
+    if constexpr (sizeof(T) == 4) {
+        if (vin) {
+            if (n >= 16) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j * row] = x[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (j < n) o[j * row] = x[j];
+            }
+        }
+    } else {
+        const bool odd = lane & 1;
+        Pack<T, 2> w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? x[2 * j] : x[2 * j + 1], 1);
+            w[j].v[0] = from_f<T>(odd ? other : x[2 * j]);
+            w[j].v[1] = from_f<T>(odd ? x[2 * j + 1] : other);
+        }
+        if (odd) {   // the odd lane has the second token of each pair
+            o += row - 1;
+            --n;
+        }
+        if (vin) {
+            if (n >= 15) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) *reinterpret_cast<Pack<T, 2> *>(o + 2 * j * row) = w[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (2 * j < n) *reinterpret_cast<Pack<T, 2> *>(o + 2 * j * row) = w[j];
+            }
+        }
+    }
 }
 
 template <typename T, int DKT>
-struct ChainSmem {
-    static constexpr int kImg = kC * DKT * 2;                                    // one part of K or Q
-    static constexpr int kStage = 2 * Parts<T>::n * kImg + kUnitBytes;           // K, Q, [T; PT], factors
-    static constexpr int kBars = 256;
-    static constexpr int kStages = 2 * kStage + kBars <= 232448 ? 2 : 1;
-    static constexpr int kBytes = kStages * kStage + kBars;
-    static_assert(kBytes <= 232448, "shared memory of a block");
-};
-
-enum { bFull = 0, bEmpty = 2, bS = 4, bR, bE, bO, bM1, bM2, bM2o, bM3, bCount };
-
-template <typename T, int DKT>
 __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, const float *init, float *last,
-                                                               const unsigned char *ws, float *keep_s, float *keep_e,
-                                                               unsigned *flags) {
-    using L = ChainSmem<T, DKT>;
-    constexpr int NB = Parts<T>::n, ST = L::kStages, HC = DKT / 2;
+                                                               const unsigned char *ws,
+                                                               const unsigned char *images, float *keep_s,
+                                                               float *keep_e, unsigned *flags) {
+    using L = Stage<T, DKT>;
+    constexpr int NB = Parts<T>::n, HC = DKT / 2, NS = DKT / 32;   // NS: K steps of a half of the state
     extern __shared__ __align__(1024) unsigned char smem[];
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + ST * L::kStage);
+    const int ST = L::count(a.dv), stage_bytes = L::bytes(a.dv);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + ST * stage_bytes);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + bCount);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int hv = blockIdx.x % a.hv, s = blockIdx.x / a.hv, hk = hv / (a.hv / a.hk);
     const Seq sq = sequence(a, s);
-    const int chunks = (sq.len + kC - 1) / kC;
+    const int chunks = uniform((sq.len + kC - 1) / kC);
 
     if (warp == 0) umma::tmem_alloc(tslot, 512);
     if (tid == 0) {
@@ -81,157 +130,158 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    const uint32_t tm = *tslot;
+    const uint32_t tm = uniform(*tslot);
     bool ok = true;
 
-    if (warp >= kEpiWarps + 1) {
+    if (warp > kEpiWarps) {
         // ------------------------------------------------------ loading ----
-        const int w = warp - kEpiWarps - 1, lt = w * 32 + lane;
-        for (int c = 0; c < chunks && ok; ++c) {
-            const int st = c % ST, turn = c / ST;
-            unsigned char *sp = smem + st * L::kStage;
+        const int lt = tid - (kEpiWarps + 1) * 32;
+        for (int c = 0, st = 0, turn = 0; c < chunks; ++c) {
+            unsigned char *sp = smem + st * stage_bytes;
             const long long tok = sq.tok0 + (long long)c * kC;
             const int rows = sq.len - c * kC < kC ? sq.len - c * kC : kC;
-            constexpr int kUnits = 2 * (kC / 8) * (DKT / 32), kBatch = 4;   // K then Q; 8 rows x 4 column groups
-            // the next chunk's V on its way to L2: the element-wise warps read it from there
-            for (int r = lt; r < kC; r += kLoadWarps * 32)
-                if (c * kC + kC + r < sq.len) {
-                    const char *p = (const char *)((const T *)a.v + (tok + kC + r) * a.sv + (long long)hv * a.dv);
-                    for (int b = 0; b < a.dv * (int)sizeof(T); b += 128)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + b));
+            const T *vp = (const T *)a.v + tok * a.sv + (long long)hv * a.dv;
+            const unsigned char *up = ws + (size_t)((sq.slot0 + c) * a.hv + hv) * kUnitBytes;
+            const unsigned char *ip = images + (size_t)((sq.slot0 + c) * a.hk + hk) * L::kTp;
+            if (c + 1 < chunks) {   // the next chunk on its way to L2
+                if (lt < kC && lt < sq.len - (c + 1) * kC) {
+                    const char *p = (const char *)(vp + (kC + lt) * a.sv);
+                    for (int i = 0; i < a.dv * (int)sizeof(T); i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
                 }
-            bool waited = false;
-            for (int u0 = w; u0 < kUnits; u0 += kLoadWarps * kBatch) {
-                uint4 p[kBatch][NB];
-#pragma unroll
-                for (int n = 0; n < kBatch; ++n) {
-                    const int u = u0 + n * kLoadWarps;
-                    const int row = (u / (DKT / 32)) % (kC / 8) * 8 + (lane & 7), cg = (u % (DKT / 32)) * 4 + (lane >> 3);
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) p[n][i] = make_uint4(0, 0, 0, 0);
-                    if (u < kUnits && row < rows && 8 * cg < a.dk) {
-                        const T *src = u < kUnits / 2 ? (const T *)a.k + (tok + row) * a.sk
-                                                      : (const T *)a.q + (tok + row) * a.sq;
-                        load_parts(src + (long long)hk * a.dk + 8 * cg, p[n]);
-                    }
-                }
-                if (!waited) {   // the stage is free (its first use needs no wait)
-                    waited = true;
-                    ok = umma::mbar_wait(bars + bEmpty + st, (turn & 1) ^ 1, kSpinLimit);
-                    if (!ok) break;
-                    if (lt == 0) {
-                        mbar_expect(bars + bFull + st, kUnitBytes);
-                        bulk_load(sp + 2 * NB * L::kImg,
-                                  ws + (size_t)((sq.slot0 + c) * a.hv + hv) * kUnitBytes, kUnitBytes,
-                                  bars + bFull + st);
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < kBatch; ++n) {
-                    const int u = u0 + n * kLoadWarps;
-                    if (u >= kUnits) break;
-                    const int row = (u / (DKT / 32)) % (kC / 8) * 8 + (lane & 7), cg = (u % (DKT / 32)) * 4 + (lane >> 3);
-#pragma unroll
-                    for (int i = 0; i < NB; ++i)
-                        *reinterpret_cast<uint4 *>(sp + ((u < kUnits / 2 ? 0 : NB) + i) * L::kImg + (row >> 3) * 128 +
-                                                   cg * 1024 + (row & 7) * 16) = p[n][i];
+                if (lt == kC) {
+                    bulk_prefetch(up + (size_t)a.hv * kUnitBytes, kUnitBytes);
+                    bulk_prefetch(ip + (size_t)a.hk * L::kTp, L::kTp);
                 }
             }
+            ok = umma::mbar_wait(bars + bEmpty + st, (turn & 1) ^ 1, kSpinLimit);   // the first use needs no wait
             if (!ok) break;
-            umma::fence_proxy_async();
-            mbar_arrive(bars + bFull + st);
+            if (lt == 0) {
+                mbar_expect(bars + bFull + st, kUnitBytes + L::kTp);
+                bulk_load(sp, ip, L::kTp, bars + bFull + st);
+                bulk_load(sp + L::kTp, up, kUnitBytes, bars + bFull + st);
+                mbar_arrive(bars + bFull + st);
+            }
+            load_rows<T>(sp + L::kV, vp, a.sv, rows, a.dv, lt, kLoadWarps * 32, bars + bFull + st);
+            if (++st == ST) {
+                st = 0;
+                ++turn;
+            }
         }
         // every copy has been waited for by the readers, unless a wait ran out: then here
-        if (!ok && lt == 0)
+        if (!ok)
             for (int i = 0; i < ST; ++i) umma::mbar_wait(bars + bFull + i, 0, 1u << 16);
     } else if (warp == kEpiWarps) {
         // ----------------------------------------------------- products ----
-        for (int c = 0; c < chunks && ok; ++c) {
-            const int st = c % ST, par = (c / ST) & 1, pc = c & 1;
-            const uint32_t k0 = saddr(smem + st * L::kStage), q0 = k0 + NB * L::kImg, t0 = k0 + 2 * NB * L::kImg;
-            ok = umma::mbar_wait(bars + bFull + st, par, kSpinLimit) && umma::mbar_wait(bars + bS, pc, kSpinLimit) &&
+        // A K step's products start as soon as the threads have written its
+        // parts; within a step the smallest parts' products come first. What
+        // the next step waits for goes first, Q's and PT's products into the
+        // gaps.
+        const uint32_t base = saddr(smem);
+        for (int c = 0, st = 0, turn = 0; c < chunks && ok; ++c) {
+            const int pc = c & 1;
+            const uint32_t k0 = base + st * stage_bytes, t0 = k0 + L::kTp;
+            // S0^T K^T (row0 = 0) or S0^T Q^T (64): steps n and NS + n
+            auto state_times = [&](uint32_t d, int row0, int n) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int o = 2; o >= 0; --o)
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) {
+                            if (o - j < 0) continue;
+                            const int ks = h * NS + n, p = o - j;
+                            mma_ts(tm + d, tm + (p < 2 ? kTmS + 16 * ks + 8 * p : kTmSl + 8 * ks),
+                                   desc_k(k0 + j * L::kImg + ks * 4096 + row0 * 16, 2048, 128),
+                                   idesc(kC, false, false), n + h > 0 || o < 2 || j > 0);
+                        }
+            };
+            // R^T T^T (pt = 0) or R^T PT^T (1): steps n and 2 + n, which meet rows 16 ks and up
+            auto r_times = [&](uint32_t d, int pt, int n) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int o = 2; o >= 0; --o)
+#pragma unroll
+                        for (int j = 0; j <= o; ++j) {
+                            const int ks = 2 * h + n, p = o - j;
+                            mma_ts(tm + d + 16 * ks, tm + (p < 2 ? kTmK + 16 * ks + 8 * p : kTmRl + 8 * ks),
+                                   desc_k(t0 + j * kTpImage + tp_offset(ks) + pt * tp_rows(ks), tp_group(ks), 128),
+                                   idesc(kC - 16 * ks, false, false), n + h > 0 || o < 2 || j > 0);
+                        }
+            };
+            ok = umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit) &&
                  (c == 0 || umma::mbar_wait(bars + bM2o, pc ^ 1, kSpinLimit));   // R's parts have been read
-            if (!ok) break;
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                ok = ok && umma::mbar_wait(bars + bS + n, pc, kSpinLimit);
+                umma::fence_after_sync();
+                if (ok && elect()) {
+                    state_times(kTmK, 0, n);
+                    if (n == NS - 1) umma::commit(bars + bM1);
+                }
+                __syncwarp();
+            }
+            ok = ok && (c == 0 || umma::mbar_wait(bars + bO, pc ^ 1, kSpinLimit));   // the last output's terms have been read
             umma::fence_after_sync();
-            auto state_times = [&](uint32_t d, uint32_t img) {   // D = S0^T (K or Q)^T
-                bool acc = false;
+            if (ok && elect())
 #pragma unroll
-                for (int o = 2; o >= 0; --o)
+                for (int n = 0; n < NS / 2; ++n) state_times(kTmQ, kC, n);
+            __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < NB; ++j) {
-                        if (o - j < 0) continue;
+            for (int n = 0; n < 2; ++n) {
+                ok = ok && umma::mbar_wait(bars + bR + n, pc, kSpinLimit);
+                umma::fence_after_sync();
+                if (ok && elect()) {
+                    r_times(kTmE, 0, n);
+                    if (n == 1) {
+                        umma::commit(bars + bM2);
 #pragma unroll
-                        for (int ks = 0; ks < DKT / 16; ++ks) {
-                            mma_ts(tm + d, tm + kTmS + part_col<DKT>(o - j, ks),
-                                   desc_k(img + j * L::kImg + ks * 2048, 1024, 128), idesc(kC, false, false), acc);
-                            acc = true;
-                        }
+                        for (int i = NS / 2; i < NS; ++i) state_times(kTmQ, kC, i);
+                        umma::commit(bars + bMq);
                     }
-            };
-            // D = R^T T^T or R^T PT^T (rows from `row0`); both are lower
-            // triangular, so K step ks meets rows 16 ks and up only
-            auto r_times = [&](uint32_t d, int row0) {
-                bool acc = false;
-#pragma unroll
-                for (int o = 2; o >= 0; --o)
-#pragma unroll
-                    for (int j = 0; j <= o; ++j)
-#pragma unroll
-                        for (int ks = 0; ks < kC / 16; ++ks) {
-                            mma_ts(tm + d + 16 * ks, tm + kTmR + part_col<kC>(o - j, ks),
-                                   desc_k(t0 + j * kTpImage + ks * 4096 + (row0 / 8 + 2 * ks) * 128, 2048, 128),
-                                   idesc(kC - 16 * ks, false, false), acc || ks > 0);
-                            if (ks == kC / 16 - 1) acc = true;
-                        }
-            };
-            if (lane == 0) {
-                state_times(kTmR, k0);
-                umma::commit(bars + bM1);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            // D1q and D2o of the chunk before have been read
-            ok = c == 0 || umma::mbar_wait(bars + bO, pc ^ 1, kSpinLimit);
-            if (!ok) break;
-            umma::fence_after_sync();
-            if (lane == 0) state_times(kTmQ, q0);
-            __syncwarp();
-            ok = umma::mbar_wait(bars + bR, pc, kSpinLimit);
-            if (!ok) break;
-            umma::fence_after_sync();
-            if (lane == 0) {
-                r_times(kTmE, 0);
-                umma::commit(bars + bM2);
-            }
-            __syncwarp();
-            ok = umma::mbar_wait(bars + bE, pc, kSpinLimit);
-            if (!ok) break;
-            umma::fence_after_sync();
-            if (lane == 0) {   // D3 = (beta e^(G_C - G) E)^T K, in the place of the state's parts
-                bool acc = false;
+            // D3 = (beta e^(G_C - G) E)^T K, in the place of the state's parts
 #pragma unroll
-                for (int o = 2; o >= 0; --o)
+            for (int n = 0; n < 2; ++n) {
+                ok = ok && umma::mbar_wait(bars + bE + n, pc, kSpinLimit);
+                if (n == 0) ok = ok && umma::mbar_wait(bars + bMq, pc, kSpinLimit);   // the state's parts have been read
+                umma::fence_after_sync();
+                if (ok && elect()) {
 #pragma unroll
-                    for (int j = 0; j < NB; ++j) {
-                        if (o - j < 0) continue;
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int ks = 0; ks < kC / 16; ++ks) {
-                            mma_ts(tm + kTmS, tm + kTmE + part_col<kC>(o - j, ks),
-                                   desc_mn(k0 + j * L::kImg + ks * 256, 128, 1024), idesc(DKT, false, true), acc);
-                            acc = true;
-                        }
+                        for (int o = 2; o >= 0; --o)
+#pragma unroll
+                            for (int j = 0; j < NB; ++j) {
+                                if (o - j < 0) continue;
+                                const int ks = 2 * h + n, p = o - j;
+                                mma_ts(tm + kTmS, tm + (p < 2 ? kTmE + 16 * ks + 8 * p : kTmEl + 8 * ks),
+                                       desc_mn(k0 + j * L::kImg + ks * 256, 128, 2048), idesc(DKT, false, true),
+                                       n + h > 0 || o < 2 || j > 0);
+                            }
+                    if (n == 1) {
+                        umma::commit(bars + bM3);
+                        r_times(kTmO, 1, 0);
+                        r_times(kTmO, 1, 1);
+                        umma::commit(bars + bM2o);
+                        umma::commit(bars + bEmpty + st);
                     }
-                umma::commit(bars + bM3);
-                r_times(kTmO, kC);
-                umma::commit(bars + bM2o);
-                umma::commit(bars + bEmpty + st);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (++st == ST) {
+                st = 0;
+                ++turn;
+            }
         }
     } else {
         // ------------------------------------------------- element-wise ----
         const int h = warp >> 2, v = (warp & 3) * 32 + lane;   // half of the columns, value channel
         const uint32_t mine = tm + ((uint32_t)((warp & 3) * 32) << 16);
         const bool vin = v < a.dv;
+        const long long orow = (long long)a.hv * a.dv;
         float S[HC];
         const size_t st0 = ((size_t)s * a.hv + hv) * a.dk * a.dv + v;
 #pragma unroll
@@ -239,37 +289,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
             const int d = h * HC + i;
             S[i] = init && vin && d < a.dk ? __ldg(init + st0 + (size_t)d * a.dv) : 0.0f;
         }
-        auto put_state = [&]() {
-#pragma unroll
-            for (int i = 0; i < HC; i += 16) {
-                float x[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = S[i + j];
-                tm_split16(mine + kTmS + part_col<DKT>(0, (h * HC + i) / 16),
-                           mine + kTmS + part_col<DKT>(1, (h * HC + i) / 16),
-                           mine + kTmS + part_col<DKT>(2, (h * HC + i) / 16), x);
-            }
+        auto done = [&](int bar) {   // this warp's tensor-memory writes (and reads) before the barrier
             tm_wait_st();
             umma::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars + bS);
+            if (lane == 0) mbar_arrive(bars + bar);
         };
-        auto put_output = [&](int c) {   // O of chunk c, once PT R has arrived
-            const int st = c % ST;
-            const float *eg = reinterpret_cast<const float *>(smem + st * L::kStage + 2 * NB * L::kImg + kTpBytes);
+        auto put_state = [&]() {
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = S[16 * n + j];
+                tm_split16(mine + kTmS + 16 * (h * NS + n), mine + kTmSl + 8 * (h * NS + n), x);
+                done(bS + n);
+            }
+        };
+        // O^T = scale e^G S0^T Q^T + (PT R)^T of chunk c, in stage st
+        auto put_output = [&](int c, int st) {
+            const int rows = sq.len - c * kC < kC ? sq.len - c * kC : kC;
+            const float *eg = reinterpret_cast<const float *>(smem + st * stage_bytes + L::kTp + kTpBytes);
             ok = umma::mbar_wait(bars + bM2o, c & 1, kSpinLimit) && ok;
             umma::fence_after_sync();
 #pragma unroll
-            for (int i = 0; i < kC / 2; i += 16) {
-                const int j0 = h * (kC / 2) + i;
-                float x[16], y[16];
+            for (int n = 0; n < 2; ++n) {
+                const int j0 = h * (kC / 2) + 16 * n;
+                float x[16], y[16], e[16];
+                get16(eg + j0, e);
                 tm_ld16(mine + kTmQ + j0, x);
                 tm_ld16(mine + kTmO + j0, y);
-                T *o = (T *)a.o + ((sq.tok0 + (long long)c * kC + j0) * a.hv + hv) * a.dv + v;
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (vin && c * kC + j0 + j < sq.len)
-                        o[(size_t)j * a.hv * a.dv] = from_f<T>(fmaf(a.scale * eg[j0 + j], x[j], y[j]));
+                for (int j = 0; j < 16; ++j) x[j] = fmaf(a.scale * e[j], x[j], y[j]);
+                store16<T>((T *)a.o + (sq.tok0 + (long long)c * kC + j0) * orow + (long long)hv * a.dv + v, orow, x,
+                           lane, vin, rows - j0);
             }
             umma::fence_before_sync();
             __syncwarp();
@@ -279,87 +331,61 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
             }
         };
         if (chunks) put_state();
-        for (int c = 0; c < chunks && ok; ++c) {
-            const int st = c % ST, pc = c & 1;
-            const float *eg = reinterpret_cast<const float *>(smem + st * L::kStage + 2 * NB * L::kImg + kTpBytes);
+        int before = 0;
+        for (int c = 0, st = 0, turn = 0; c < chunks; ++c) {
+            const int pc = c & 1;
+            const unsigned char *sp = smem + st * stage_bytes;
+            const float *eg = reinterpret_cast<const float *>(sp + L::kTp + kTpBytes);
+            // lanes past dv compute what channel 0 would be; nothing of it is stored
+            const T *vs = reinterpret_cast<const T *>(sp + L::kV) + (vin ? v : 0);
             const long long unit = (sq.slot0 + c) * a.hv + hv;
-            T vr[kC / 2];   // V^T of this thread's tokens, on its way while the output is written
-            {
-                const T *vp = (const T *)a.v + (sq.tok0 + (long long)c * kC + h * (kC / 2)) * a.sv +
-                              (long long)hv * a.dv + v;
-#pragma unroll
-                for (int j = 0; j < kC / 2; ++j)
-                    vr[j] = vin && c * kC + h * (kC / 2) + j < sq.len ? vp[(long long)j * a.sv] : from_f<T>(0.0f);
-            }
             if (keep_s && vin) {   // the state before the chunk
                 float *ks = keep_s + (size_t)unit * a.dk * a.dv + v;
 #pragma unroll
                 for (int i = 0; i < HC; ++i)
                     if (h * HC + i < a.dk) ks[(size_t)(h * HC + i) * a.dv] = S[i];
             }
-            if (c > 0) put_output(c - 1);
-            ok = ok && umma::mbar_wait(bars + bFull + st, (c / ST) & 1, kSpinLimit) &&
+            if (c > 0) put_output(c - 1, before);
+            ok = ok && umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit) &&
                  umma::mbar_wait(bars + bM1, pc, kSpinLimit);
             if (!ok) break;
             umma::fence_after_sync();
 #pragma unroll
-            for (int i = 0; i < kC / 2; i += 16) {   // R^T = V^T - e^G D1k
-                const int j0 = h * (kC / 2) + i;
-                float x[16];
-                tm_ld16(mine + kTmR + j0, x);
+            for (int n = 0; n < 2; ++n) {   // R^T = V^T - e^G S0^T K^T
+                const int j0 = h * (kC / 2) + 16 * n;
+                float x[16], e[16], r[16];
+                get16(eg + j0, e);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = fmaf(-eg[j0 + j], x[j], to_f(vr[i + j]));
-                // the parts go where this half's accumulators were: both groups are read before either is written
-                if (i == 0) {
-                    float y[16];
-                    tm_ld16(mine + kTmR + j0 + 16, y);
+                for (int j = 0; j < 16; ++j) r[j] = to_f(vs[(j0 + j) * a.dv]);
+                tm_ld16(mine + kTmK + j0, x);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] = fmaf(-eg[j0 + 16 + j], y[j], to_f(vr[16 + j]));
-                    tm_split16(mine + kTmR + part_col<kC>(0, j0 / 16), mine + kTmR + part_col<kC>(1, j0 / 16),
-                               mine + kTmR + part_col<kC>(2, j0 / 16), x);
-                    tm_split16(mine + kTmR + part_col<kC>(0, j0 / 16 + 1), mine + kTmR + part_col<kC>(1, j0 / 16 + 1),
-                               mine + kTmR + part_col<kC>(2, j0 / 16 + 1), y);
-                    break;
-                }
+                for (int j = 0; j < 16; ++j) x[j] = fmaf(-e[j], x[j], r[j]);
+                tm_split16(mine + kTmK + j0, mine + kTmRl + j0 / 2, x);
+                done(bR + n);
             }
-            tm_wait_st();
-            umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars + bR);
             ok = umma::mbar_wait(bars + bM2, pc, kSpinLimit);
             if (!ok) break;
             umma::fence_after_sync();
-            {   // E^T, and beta e^(G_C - G) E as the next operand
-                const int j0 = h * (kC / 2);
-                float x[16], y[16];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {   // E^T, and beta e^(G_C - G) E as the next operand
+                const int j0 = h * (kC / 2) + 16 * n;
+                float x[16], e[16];
+                get16(eg + kC + j0, e);
                 tm_ld16(mine + kTmE + j0, x);
-                tm_ld16(mine + kTmE + j0 + 16, y);
                 if (keep_e && vin) {
                     float *ke = keep_e + ((size_t)unit * kC + j0) * a.dv + v;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        ke[(size_t)j * a.dv] = x[j];
-                        ke[(size_t)(j + 16) * a.dv] = y[j];
-                    }
+                    for (int j = 0; j < 16; ++j) ke[(size_t)j * a.dv] = x[j];
                 }
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    x[j] *= eg[kC + j0 + j];
-                    y[j] *= eg[kC + j0 + 16 + j];
-                }
-                tm_split16(mine + kTmE + part_col<kC>(0, j0 / 16), mine + kTmE + part_col<kC>(1, j0 / 16),
-                           mine + kTmE + part_col<kC>(2, j0 / 16), x);
-                tm_split16(mine + kTmE + part_col<kC>(0, j0 / 16 + 1), mine + kTmE + part_col<kC>(1, j0 / 16 + 1),
-                           mine + kTmE + part_col<kC>(2, j0 / 16 + 1), y);
+                for (int j = 0; j < 16; ++j) x[j] *= e[j];
+                tm_split16(mine + kTmE + j0, mine + kTmEl + j0 / 2, x);
+                done(bE + n);
             }
-            tm_wait_st();
-            umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars + bE);
+            const float total = eg[kC - 1];   // e^(G_C): rows past the end have g = 0
             ok = umma::mbar_wait(bars + bM3, pc, kSpinLimit);
             if (!ok) break;
             umma::fence_after_sync();
-            const float total = eg[kC - 1];   // e^(G_C): rows past the end have g = 0
 #pragma unroll
             for (int i = 0; i < HC; i += 16) {
                 float x[16];
@@ -368,8 +394,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 for (int j = 0; j < 16; ++j) S[i + j] = fmaf(total, S[i + j], x[j]);
             }
             if (c + 1 < chunks) put_state();
+            before = st;
+            if (++st == ST) {
+                st = 0;
+                ++turn;
+            }
         }
-        if (ok && chunks) put_output(chunks - 1);
+        if (ok && chunks) put_output(chunks - 1, before);
         if (last && vin) {
 #pragma unroll
             for (int i = 0; i < HC; ++i)
@@ -377,8 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
         }
     }
     if (!ok && flags && lane == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
-    // a wait that ran out may leave products in flight
-    if (warp == kEpiWarps && !ok) {
+    if (warp == kEpiWarps && !ok) {   // a wait that ran out may leave products in flight
         if (lane == 0) umma::commit(bars + bM3);
         __syncwarp();
         umma::mbar_wait(bars + bM3, 0, 1u << 16);
@@ -393,11 +423,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
 template <typename T, int DKT>
 cudaError_t run(const DeltaArgs &a, const float *init, float *last, const void *ws, float *keep_s, float *keep_e,
                 unsigned *flags, cudaStream_t st) {
-    constexpr int smem = ChainSmem<T, DKT>::kBytes;
+    const int smem = Stage<T, DKT>::count(a.dv) * Stage<T, DKT>::bytes(a.dv) + 256;
     cudaError_t e = cudaFuncSetAttribute(k_delta_forward<T, DKT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    k_delta_forward<T, DKT><<<a.n * a.hv, kThreads, smem, st>>>(a, init, last, (const unsigned char *)ws, keep_s,
-                                                                keep_e, flags);
+    const unsigned char *units = (const unsigned char *)ws;
+    k_delta_forward<T, DKT><<<a.n * a.hv, kThreads, smem, st>>>(
+        a, init, last, units, units + (size_t)slots(a.tokens, a.n) * a.hv * kUnitBytes, keep_s, keep_e, flags);
     return cudaGetLastError();
 }
 

@@ -16,30 +16,67 @@ namespace {
 using namespace delta;
 
 constexpr int kLd = kC + 4;   // row stride of the float matrices: 16-byte rows, shifted banks
+constexpr int kMat = kC * kLd * 4;
+constexpr int kTImg = kC * kC * 2;   // one part of T, 64 x 64
 
+// where row r of T (pt = 0) or PT (1), column group cg of a packed part lies; r / 16 >= cg / 2
+__device__ __forceinline__ int packed(int r, int cg, int pt) {
+    const int ks = cg >> 1, pr = r - 16 * ks;
+    return tp_offset(ks) + (cg & 1) * tp_group(ks) + pt * tp_rows(ks) + (pr >> 3) * 128 + (pr & 7) * 16;
+}
+
+// Shared memory: the images of [K; Q], in whose place T (float) and behind it
+// T's parts come later; A D_b (float) behind the images, which the parts may
+// overwrite when T is done.
 template <typename T, int DKT>
 struct PrepSmem {
-    static constexpr int kKq = Parts<T>::n * 2 * kC * DKT * 2;   // images of [K; Q], 128 rows
-    static constexpr int kTImg = kC * kC * 2;                    // one part of T, 64 x 64
-    static constexpr int kFloat = 2 * kC * kLd * 4;              // A D_b, T
-    static constexpr int kImg = kKq > 3 * kTImg ? kKq : 3 * kTImg;   // T's images take the place of K's and Q's
-    static constexpr int kBytes = kImg + kFloat + kC * 8 + 2 * kC * 4 + 64;
+    static constexpr int kImg = kq_bytes<T, DKT>() > kMat ? kq_bytes<T, DKT>() : kMat;
+    static constexpr int kParts = kMat + 3 * kTImg;
+    static constexpr int kBig = kImg + kMat > kParts ? kImg + kMat : kParts;
+    static constexpr int kBytes = kBig + kC * 8 + 3 * kC * 4 + 64;
 };
 
+// D[m x n] (rows r0, columns c0 of Y) = sign * X[m x k] Z[k x n] for float matrices of row stride kLd; 4 columns of one
+// row a thread and pass
+template <int M, int N, int K, bool NEG, typename FY>
+__device__ __forceinline__ void small_product(const float *X, const float *Z, int t, int nt, FY &&put) {
+    for (int i = t; i < M * N / 4; i += nt) {
+        const int r = i / (N / 4), c = i % (N / 4) * 4;
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < K; k += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(X + r * kLd + k);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 z = *reinterpret_cast<const float4 *>(Z + (k + j) * kLd + c);
+                const float v = NEG ? -xs[j] : xs[j];
+                y.x = fmaf(v, z.x, y.x);
+                y.y = fmaf(v, z.y, y.y);
+                y.z = fmaf(v, z.z, y.z);
+                y.w = fmaf(v, z.w, y.w);
+            }
+        }
+        put(r, c, y);
+    }
+}
+
 template <typename T, int DKT>
-__global__ void __launch_bounds__(128) k_delta_prep(DeltaArgs a, unsigned char *ws, unsigned *flags) {
+__global__ void __launch_bounds__(128, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : PrepSmem<T, DKT>::kBytes < 76000 ? 3 : 2)
+    k_delta_prep(DeltaArgs a, unsigned char *ws, unsigned char *images, unsigned *flags) {
     using L = PrepSmem<T, DKT>;
-    constexpr int NB = Parts<T>::n;
+    constexpr int NB = Parts<T>::n, kPart = 2 * kC * DKT * 2;
     extern __shared__ __align__(1024) unsigned char smem[];
-    float *As = reinterpret_cast<float *>(smem + L::kImg), *Ts = As + kC * kLd;
-    double *Gs = reinterpret_cast<double *>(Ts + kC * kLd);
-    float *gs = reinterpret_cast<float *>(Gs + kC), *bs = gs + kC;
-    uint64_t *bar = reinterpret_cast<uint64_t *>(bs + kC);
+    float *Ts = reinterpret_cast<float *>(smem), *As = reinterpret_cast<float *>(smem + L::kImg);
+    unsigned char *parts = smem + kMat;
+    double *Gs = reinterpret_cast<double *>(smem + L::kBig);
+    float *cs = reinterpret_cast<float *>(Gs + kC), *bs = cs + kC;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(bs + 2 * kC);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
     const long long slot = blockIdx.x / a.hv;
-    const int hv = blockIdx.x % a.hv, hk = hv / (a.hv / a.hk);
+    const int hv = blockIdx.x % a.hv, per = a.hv / a.hk, hk = hv / per;
     int s = 0;   // the last sequence that starts at or before the slot
     for (int lo = 0, hi = a.n; lo < hi;) {
         const int m = (lo + hi) >> 1;
@@ -56,116 +93,117 @@ __global__ void __launch_bounds__(128) k_delta_prep(DeltaArgs a, unsigned char *
     const int rows = sq.len - c0 < kC ? (int)(sq.len - c0) : kC;
     const long long tok = sq.tok0 + c0;
 
-    if (warp == 0) umma::tmem_alloc(tslot, 256);
+    load_image<T, DKT>(smem, kPart, 2048, (const T *)a.k + tok * a.sk + (long long)hk * a.dk, a.sk, rows, a.dk, warp, 4);
+    load_image<T, DKT>(smem + 1024, kPart, 2048, (const T *)a.q + tok * a.sq + (long long)hk * a.dk, a.sq, rows, a.dk,
+                       warp, 4);
+    if (warp == 0) umma::tmem_alloc(tslot, 128);
     if (tid == 0) {
         umma::mbar_init(bar, 1);
         umma::fence_mbar_init();
-    }
-    {   // [K; Q] into the images: a warp takes 8 rows x 4 column groups at a time
-        constexpr int kUnits = 16 * (DKT / 32);
-        for (int u = warp; u < kUnits; u += 4) {
-            const int r = (u / (DKT / 32)) * 8 + (lane & 7), cg = (u % (DKT / 32)) * 4 + (lane >> 3);
-            const int row = r & (kC - 1);
-            uint4 p[NB];
-#pragma unroll
-            for (int i = 0; i < NB; ++i) p[i] = make_uint4(0, 0, 0, 0);
-            if (row < rows && 8 * cg < a.dk) {
-                const T *src = r < kC ? (const T *)a.k + (tok + row) * a.sk : (const T *)a.q + (tok + row) * a.sq;
-                load_parts(src + (long long)hk * a.dk + 8 * cg, p);
-            }
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-                *reinterpret_cast<uint4 *>(smem + i * (2 * kC * DKT * 2) + (r >> 3) * 128 + cg * 2048 + (r & 7) * 16) =
-                    p[i];
-        }
     }
     if (warp == 1) {   // running sums of g in double: differences of large sums keep float's accuracy
         const int j = 2 * lane;
         const long long at = tok * a.hv + hv;
         float g0 = j < rows ? __ldg(a.g + at + (long long)j * a.hv) : 0.0f;
         float g1 = j + 1 < rows ? __ldg(a.g + at + (long long)(j + 1) * a.hv) : 0.0f;
+        const float b0 = j < rows ? __ldg(a.beta + at + (long long)j * a.hv) : 0.0f;
+        const float b1 = j + 1 < rows ? __ldg(a.beta + at + (long long)(j + 1) * a.hv) : 0.0f;
         // exp(-1e5) is 0 as exp(-inf) is, and differences stay numbers
         g0 = g0 < -1e5f ? -1e5f : g0;
         g1 = g1 < -1e5f ? -1e5f : g1;
-        double x = (double)g0 + (double)g1, y = x;
+        double y = (double)g0 + (double)g1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double z = __shfl_up_sync(0xffffffffu, y, o);
             if (lane >= o) y += z;
         }
-        Gs[j] = y - (double)g1;
+        const double x = y - (double)g1;
+        Gs[j] = x;
         Gs[j + 1] = y;
-        bs[j] = j < rows ? __ldg(a.beta + at + (long long)j * a.hv) : 0.0f;
-        bs[j + 1] = j + 1 < rows ? __ldg(a.beta + at + (long long)(j + 1) * a.hv) : 0.0f;
+        bs[j] = b0;
+        bs[j + 1] = b1;
+        // beta_j e^(G at the end of j's 16 tokens - G_j); the factor e^(G_i - G at that end) is the row's
+        const double end = __shfl_sync(0xffffffffu, y, lane | 7), all = __shfl_sync(0xffffffffu, y, 31);
+        cs[j] = b0 * expf((float)(end - x));
+        cs[j + 1] = b1 * expf((float)(end - y));
+        float *fac = reinterpret_cast<float *>(ws + (size_t)blockIdx.x * kUnitBytes + kTpBytes);
+        *reinterpret_cast<float2 *>(fac + j) = make_float2(expf((float)x), expf((float)y));
+        *reinterpret_cast<float2 *>(fac + kC + j) =
+            make_float2(b0 * expf((float)(all - x)), b1 * expf((float)(all - y)));
     }
+    umma::cp_async_wait_all();
     umma::fence_proxy_async();
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    const uint32_t tm = *tslot;
-    uint32_t phase = 0;
+    const uint32_t tm = uniform(*tslot), base = saddr(smem);
     bool ok = true;
-    if (tid == 0) {
-        const uint32_t base = saddr(smem);
-        bool acc = false;
+    if (warp == 0) {
+        if (elect()) {
+            bool acc = false;
 #pragma unroll
-        for (int o = 2; o >= 0; --o)   // parts' products, the smallest first
+            for (int o = 2; o >= 0; --o)   // parts' products, the smallest first
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int j = o - i;
-                if (j < 0 || j >= NB) continue;
-                for (int ks = 0; ks < DKT / 16; ++ks) {
-                    umma::mma_bf16(tm, desc_k(base + i * (2 * kC * DKT * 2) + ks * 4096, 2048, 128),
-                                   desc_k(base + j * (2 * kC * DKT * 2) + ks * 4096, 2048, 128), idesc(kC, false, false),
-                                   acc);
-                    acc = true;
+                for (int i = 0; i < NB; ++i) {
+                    const int j = o - i;
+                    if (j < 0 || j >= NB) continue;
+#pragma unroll
+                    for (int ks = 0; ks < DKT / 16; ++ks) {
+                        umma::mma_bf16(tm, desc_k(base + i * kPart + ks * 4096, 2048, 128),
+                                       desc_k(base + j * kPart + ks * 4096, 2048, 128), idesc(kC, false, false), acc);
+                        acc = true;
+                    }
                 }
-            }
-        umma::commit(bar);
+            umma::commit(bar);
+        }
+        __syncwarp();
     }
-    ok = umma::mbar_wait(bar, phase, kSpinLimit);
-    phase ^= 1;
+    if (tid == 0 && hv % per == 0)   // the images for the chains; behind the first use of this memory for something else
+        bulk_store(images + (size_t)(slot * a.hk + hk) * kq_bytes<T, DKT>(), smem, kq_bytes<T, DKT>());
+    ok = umma::mbar_wait(bar, 0, kSpinLimit);
     umma::fence_after_sync();
     const uint32_t mine = tm + ((uint32_t)(warp * 32) << 16);
-    const int i = tid & (kC - 1);   // this thread's row of A or of P
+    const int i = tid & (kC - 1), ib = i >> 4;   // this thread's row of A (threads 0-63) or P, and its 16 tokens
+    const float mul = tid < kC ? 1.0f : a.scale;
     {
         const double Gi = Gs[i];
 #pragma unroll
         for (int c = 0; c < kC; c += 16) {
             float d[16];
             tm_ld16(mine + c, d);
-            if (tid < kC) {
+            const int last = c + 15;
+            if (c / 16 < ib) {   // all columns are earlier tokens: one factor for the row, one for each column
+                const float rf = mul * expf((float)(Gi - Gs[last]));
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    d[j] = c + j < i ? d[j] * expf((float)(Gi - Gs[c + j])) * bs[c + j] : 0.0f;
-                }
+                for (int j = 0; j < 16; ++j) d[j] *= rf * cs[c + j];
+            } else if (c / 16 == ib) {
+                const int m = tid < kC ? i : i + 1;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    d[j] = c + j < m ? d[j] * (mul * bs[c + j]) * expf((float)(Gi - Gs[c + j])) : 0.0f;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) d[j] = 0.0f;
+            }
+            if (warp < 2) {
 #pragma unroll
                 for (int j = 0; j < 16; j += 4)
                     *reinterpret_cast<float4 *>(As + i * kLd + c + j) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) d[j] = 0.0f;   // rows 0-63 of the second product's operand are not used
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    d[j] = c + j <= i ? d[j] * (a.scale * bs[c + j]) * expf((float)(Gi - Gs[c + j])) : 0.0f;
             }
-            tm_split16(mine + 64 + c / 2, mine + 96 + c / 2, mine + 128 + c / 2, d);
+            // P as operand; rows 0-63 of it are A's and their products go unread
+            tm_split16(mine + c, mine + 64 + c / 2, d);
         }
         tm_wait_st();
-        if (tid >= kC) {
-            unsigned char *fac = ws + (size_t)blockIdx.x * kUnitBytes + kTpBytes;
-            reinterpret_cast<float *>(fac)[i] = expf((float)Gi);
-            reinterpret_cast<float *>(fac)[kC + i] = bs[i] * expf((float)(Gs[kC - 1] - Gi));
-        }
     }
+    if (tid == 0) bulk_store_read();
+    umma::fence_before_sync();
     __syncthreads();
-    // T11 and T22 by columns: x_r = [r = c] - sum_{j < r} A_rj x_j
-    if (warp < 2) {
-        const int o = 32 * warp;
-        float x[32];
+    {   // the 16 x 16 diagonal blocks of T by columns, a warp each: x_r = [r = c] - sum_{j < r} A_rj x_j
+        const int o = 16 * warp, c = lane & 15;
+        float x[16];
 #pragma unroll
-        for (int r = 0; r < 32; ++r) {
-            float acc[4] = {r == lane ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r = 0; r < 16; ++r) {
+            float acc[4] = {r == c ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < r; j += 4) {
                 const float4 v = *reinterpret_cast<const float4 *>(As + (o + r) * kLd + o + j);
@@ -175,118 +213,121 @@ __global__ void __launch_bounds__(128) k_delta_prep(DeltaArgs a, unsigned char *
                 if (j + 3 < r) acc[3] = fmaf(-v.w, x[j + 3], acc[3]);
             }
             x[r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-            Ts[(o + r) * kLd + o + lane] = x[r];
         }
-    } else if (warp == 2) {   // T12 = 0
+        if (lane < 16)
 #pragma unroll
-        for (int r = 0; r < 32; ++r) Ts[r * kLd + 32 + lane] = 0.0f;
+            for (int r = 0; r < 16; ++r) Ts[(o + r) * kLd + o + c] = x[r];
     }
     __syncthreads();
-    {   // T21 = -T22 (A21 T11): row and 8 columns of it a thread
-        const int r = tid >> 2, c = (tid & 3) * 8;
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = 0.0f;
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float v = As[(32 + r) * kLd + k];
-            const float4 p = *reinterpret_cast<const float4 *>(Ts + k * kLd + c);
-            const float4 q = *reinterpret_cast<const float4 *>(Ts + k * kLd + c + 4);
-            y[0] = fmaf(v, p.x, y[0]);
-            y[1] = fmaf(v, p.y, y[1]);
-            y[2] = fmaf(v, p.z, y[2]);
-            y[3] = fmaf(v, p.w, y[3]);
-            y[4] = fmaf(v, q.x, y[4]);
-            y[5] = fmaf(v, q.y, y[5]);
-            y[6] = fmaf(v, q.z, y[6]);
-            y[7] = fmaf(v, q.w, y[7]);
-        }
-        // the rows 0-31 of A are used up: A21 T11 goes there
+    // T21 = -T22 (A21 T11), first for the two pairs of 16 x 16 blocks, then for
+    // the 32 x 32 ones; A21 T11 goes where A12 = 0 lies
+    {
+        const int o = 32 * (warp >> 1), t = tid & 63;
+        small_product<16, 16, 16, false>(As + (o + 16) * kLd + o, Ts + o * kLd + o, t, 64, [&](int r, int c, float4 y) {
+            *reinterpret_cast<float4 *>(As + (o + r) * kLd + o + 16 + c) = y;
+        });
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 8; j += 4)
-            *reinterpret_cast<float4 *>(As + r * kLd + c + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = 0.0f;
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float v = -Ts[(32 + r) * kLd + 32 + k];
-            const float4 p = *reinterpret_cast<const float4 *>(As + k * kLd + c);
-            const float4 q = *reinterpret_cast<const float4 *>(As + k * kLd + c + 4);
-            y[0] = fmaf(v, p.x, y[0]);
-            y[1] = fmaf(v, p.y, y[1]);
-            y[2] = fmaf(v, p.z, y[2]);
-            y[3] = fmaf(v, p.w, y[3]);
-            y[4] = fmaf(v, q.x, y[4]);
-            y[5] = fmaf(v, q.y, y[5]);
-            y[6] = fmaf(v, q.z, y[6]);
-            y[7] = fmaf(v, q.w, y[7]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; j += 4)
-            *reinterpret_cast<float4 *>(Ts + (32 + r) * kLd + c + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+        small_product<16, 16, 16, true>(Ts + (o + 16) * kLd + o + 16, As + o * kLd + o + 16, t, 64,
+                                        [&](int r, int c, float4 y) {
+                                            *reinterpret_cast<float4 *>(Ts + (o + 16 + r) * kLd + o + c) = y;
+                                            *reinterpret_cast<float4 *>(Ts + (o + r) * kLd + o + 16 + c) =
+                                                make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                        });
     }
+    __syncthreads();
+    small_product<32, 32, 32, false>(As + 32 * kLd, Ts, tid, 128, [&](int r, int c, float4 y) {
+        *reinterpret_cast<float4 *>(As + r * kLd + 32 + c) = y;
+    });
+    __syncthreads();
+    small_product<32, 32, 32, true>(Ts + 32 * kLd + 32, As + 32, tid, 128, [&](int r, int c, float4 y) {
+        *reinterpret_cast<float4 *>(Ts + (32 + r) * kLd + c) = y;
+    });
     __syncthreads();
     unsigned char *out = ws + (size_t)blockIdx.x * kUnitBytes;
-    {   // T's parts: into shared memory as operand (64 rows) and to the workspace (rows 0-63 of [T; PT])
+    {   // T's parts: into shared memory as operand and to the workspace
         const int r = tid & 63;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            const int cg = (tid >> 6) * 4 + n;
+            const int cg = (tid >> 6) + 2 * n;
             uint32_t w[4][3];
+            const bool in = cg <= r / 8;   // the lower triangle; columns behind the diagonal's block are not read above it
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
+            if (in) {
+                x = *reinterpret_cast<const float4 *>(Ts + r * kLd + 8 * cg);
+                y = *reinterpret_cast<const float4 *>(Ts + r * kLd + 8 * cg + 4);
+                if (cg == r / 8) {   // zeros above the diagonal
+                    float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                split<3>(Ts[r * kLd + 8 * cg + 2 * j], Ts[r * kLd + 8 * cg + 2 * j + 1], w[j]);
+                    for (int j = 0; j < 8; ++j) z[j] = j <= (r & 7) ? z[j] : 0.0f;
+                    x = make_float4(z[0], z[1], z[2], z[3]);
+                    y = make_float4(z[4], z[5], z[6], z[7]);
+                }
+            }
+            split<3>(x.x, x.y, w[0]);
+            split<3>(x.z, x.w, w[1]);
+            split<3>(y.x, y.y, w[2]);
+            split<3>(y.z, y.w, w[3]);
 #pragma unroll
             for (int q = 0; q < 3; ++q) {
                 const uint4 v = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
-                *reinterpret_cast<uint4 *>(smem + q * L::kTImg + (r >> 3) * 128 + cg * 1024 + (r & 7) * 16) = v;
-                *reinterpret_cast<uint4 *>(out + q * kTpImage + (r >> 3) * 128 + cg * 2048 + (r & 7) * 16) = v;
+                *reinterpret_cast<uint4 *>(parts + q * kTImg + (r >> 3) * 128 + cg * 1024 + (r & 7) * 16) = v;
+                if (r / 16 >= cg / 2) *reinterpret_cast<uint4 *>(out + q * kTpImage + packed(r, cg, 0)) = v;
             }
         }
     }
     umma::fence_proxy_async();
-    umma::fence_before_sync();
-    __syncthreads();
-    umma::fence_after_sync();
-    if (tid == 0) {   // PT = P' T: K runs over T's rows
-        const uint32_t base = saddr(smem);
-        bool acc = false;
+    // PT = P T, K over T's rows, 32 columns at a time (rows 32 and up for the
+    // second half), so that P's parts and the result share 128 columns
 #pragma unroll
-        for (int o = 2; o >= 0; --o)
+    for (int half = 0; half < 2; ++half) {
+        umma::fence_before_sync();
+        __syncthreads();
+        umma::fence_after_sync();
+        if (warp == 0) {
+            if (elect()) {
+                bool acc = false;
 #pragma unroll
-            for (int p = 0; p <= o; ++p)
-                for (int ks = 0; ks < kC / 16; ++ks) {
-                    mma_ts(tm, tm + 64 + 32 * p + 8 * ks, desc_mn(base + (o - p) * L::kTImg + ks * 256, 128, 1024),
-                           idesc(kC, false, true), acc);
-                    acc = true;
-                }
-        umma::commit(bar);
-    }
-    ok = umma::mbar_wait(bar, phase, kSpinLimit) && ok;
-    umma::fence_after_sync();
-    if (tid >= kC) {
+                for (int o = 2; o >= 0; --o)
 #pragma unroll
-        for (int c = 0; c < kC; c += 16) {
-            float d[16];
-            tm_ld16(mine + c, d);
+                    for (int p = 0; p <= o; ++p)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t w[4][3];
+                        for (int ks = 2 * half; ks < kC / 16; ++ks) {
+                            mma_ts(tm + 96, tm + (p < 2 ? 16 * ks + 8 * p : 64 + 8 * ks),
+                                   desc_mn(saddr(parts) + (o - p) * kTImg + ks * 256 + half * 4096, 128, 1024),
+                                   idesc(32, false, true), acc);
+                            acc = true;
+                        }
+                umma::commit(bar);
+            }
+            __syncwarp();
+        }
+        ok = umma::mbar_wait(bar, 1 ^ half, kSpinLimit) && ok;
+        umma::fence_after_sync();
+        if (warp >= 2) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) split<3>(d[8 * h + 2 * j], d[8 * h + 2 * j + 1], w[j]);
+            for (int c = 0; c < 32; c += 16) {
+                float d[16];
+                tm_ld16(mine + 96 + c, d);
+                const int cc = 32 * half + c;
+                if (ib >= cc / 16)
 #pragma unroll
-                for (int q = 0; q < 3; ++q)
-                    *reinterpret_cast<uint4 *>(out + q * kTpImage + (8 + (i >> 3)) * 128 + (c / 8 + h) * 2048 +
-                                               (i & 7) * 16) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[4][3];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) split<3>(d[8 * h + 2 * j], d[8 * h + 2 * j + 1], w[j]);
+#pragma unroll
+                        for (int q = 0; q < 3; ++q)
+                            *reinterpret_cast<uint4 *>(out + q * kTpImage + packed(i, cc / 8 + h, 1)) =
+                                make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+                    }
             }
         }
     }
     if (!ok && flags && tid == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
+    if (tid == 0) bulk_store_wait();
     umma::fence_before_sync();
     __syncthreads();
-    if (warp == 0) umma::tmem_dealloc(tm, 256);
+    if (warp == 0) umma::tmem_dealloc(tm, 128);
 }
 
 template <typename T, int DKT>
@@ -294,14 +335,24 @@ cudaError_t run(const DeltaArgs &a, void *ws, unsigned *flags, cudaStream_t st) 
     constexpr int smem = PrepSmem<T, DKT>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(k_delta_prep<T, DKT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const long long grid = slots(a.tokens, a.n) * a.hv;
-    k_delta_prep<T, DKT><<<(unsigned)grid, 128, smem, st>>>(a, (unsigned char *)ws, flags);
+    const long long units = slots(a.tokens, a.n) * a.hv;
+    k_delta_prep<T, DKT><<<(unsigned)units, 128, smem, st>>>(a, (unsigned char *)ws,
+                                                             (unsigned char *)ws + (size_t)units * kUnitBytes, flags);
     return cudaGetLastError();
+}
+
+template <typename T>
+size_t bytes(long long slots, int hk, int hv, int dk) {
+    return (size_t)slots * (hv * (size_t)kUnitBytes + hk * (size_t)(dk > 64 ? kq_bytes<T, 128>() : kq_bytes<T, 64>()));
 }
 
 }  // namespace
 
-size_t delta_unit_bytes() { return delta::kUnitBytes; }
+size_t delta_prep_bytes(int dtype, long long tokens, int n, int hk, int hv, int dk) {
+    const long long c = slots(tokens, n);
+    return dtype == S4_BF16 ? bytes<__nv_bfloat16>(c, hk, hv, dk)
+                            : dtype == S4_F16 ? bytes<__half>(c, hk, hv, dk) : bytes<float>(c, hk, hv, dk);
+}
 
 cudaError_t launch_delta_prep(int dtype, const DeltaArgs &a, void *ws, unsigned *flags, cudaStream_t st) {
     const bool wide = a.dk > 64;

@@ -109,8 +109,8 @@ struct DeltaArgs {
 // T tokens for each sequence, state [n, hv, dk, dv] in place
 cudaError_t launch_delta_scan(int dtype, const DeltaArgs &a, float *state, int T, cudaStream_t st);
 
-// bytes of the images and factors of one chunk and value head
-size_t delta_unit_bytes();
+// bytes of the images and factors of all chunks
+size_t delta_prep_bytes(int dtype, long long tokens, int n, int hk, int hv, int dk);
 // the chunks' images of T and PT and the gates' factors
 cudaError_t launch_delta_prep(int dtype, const DeltaArgs &a, void *ws, unsigned *flags, cudaStream_t st);
 // o and the last states; keep_s, keep_e (or null): the state before every chunk and E of every chunk

@@ -177,6 +177,18 @@ __device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t (&v)[8]) {
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 16 consecutive floats of shared memory (16-byte aligned, the same for the warp)
+__device__ __forceinline__ void get16(const float *p, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 f = reinterpret_cast<const float4 *>(p)[i];
+        v[4 * i] = f.x;
+        v[4 * i + 1] = f.y;
+        v[4 * i + 2] = f.z;
+        v[4 * i + 3] = f.w;
+    }
+}
+
 // 16 floats (consecutive K elements of a lane, one K step) as three parts of
 // 8 columns: the high and middle ones side by side at `at`, which is where an
 // accumulator of the same 16 columns lies, the low one at `lo`
@@ -257,16 +269,6 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 __device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
-
-// shared memory (written with a fence.proxy.async behind) to global memory; by one thread
-__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(saddr(src)), "r"(bytes)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// the thread's stores have read their source / are done
-__device__ __forceinline__ void bulk_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // `rows` rows of dv elements (zeros up to 64 rows) to consecutive places of
 // dst, by thread t of nt; done when m has this thread's arrival (one of those

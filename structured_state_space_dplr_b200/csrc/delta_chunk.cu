@@ -47,18 +47,6 @@ struct Stage {
 
 enum { bFull = 0, bEmpty = 2, bS = 4, bR = 8, bE = 10, bO = 12, bM1, bM2, bMq, bM2o, bM3, bCount };
 
-// 16 consecutive floats of shared memory (16-byte aligned, the same for the warp)
-__device__ __forceinline__ void get16(const float *p, float (&v)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 f = reinterpret_cast<const float4 *>(p)[i];
-        v[4 * i] = f.x;
-        v[4 * i + 1] = f.y;
-        v[4 * i + 2] = f.z;
-        v[4 * i + 3] = f.w;
-    }
-}
-
 // 16 tokens of this lane's channel to o, `row` elements apart, the first n of
 // them. 16-bit types: neighbouring lanes swap so that each stores two channels
 // of every other token in one word (dv is even: both channels are there or not).

@@ -2,11 +2,13 @@
 // depend on the state: for every chunk and value head the images of
 // T = (I + A D_b)^-1 and PT = P D_b T and the gates' factors.
 //
-// One block per chunk and value head, 128 threads. [K; Q] K^T is one M = 128
-// product (rows 0-63 give A, rows 64-127 give P); a thread owns a row of the
-// accumulator. T is inverted in float: the two 32 x 32 diagonal blocks by
-// forward substitution, a column a thread, then T21 = -T22 A21 T11. PT is a
-// second product with P as operand in tensor memory.
+// One block per chunk and value head. [K; Q] K^T is one M = 128 product (rows
+// 0-63 give A, rows 64-127 give P); two threads share a row of the
+// accumulator. T is inverted in float: the 16 x 16 diagonal blocks by forward
+// substitution, a column a thread, then T21 = -T22 A21 T11 twice, for blocks of
+// 16 and of 32. PT is a second product with P as operand in tensor memory.
+// Bound by the latency of these steps one after the other: four blocks of
+// eight warps share an SM (128 tensor-memory columns each).
 #include "delta.cuh"
 #include "s4dplr.h"
 
@@ -33,7 +35,7 @@ struct PrepSmem {
     static constexpr int kImg = kq_bytes<T, DKT>() > kMat ? kq_bytes<T, DKT>() : kMat;
     static constexpr int kParts = kMat + 3 * kTImg;
     static constexpr int kBig = kImg + kMat > kParts ? kImg + kMat : kParts;
-    static constexpr int kBytes = kBig + kC * 8 + 3 * kC * 4 + 64;
+    static constexpr int kBytes = kBig + 4 * kC * 4 + 64;
 };
 
 // D[m x n] (rows r0, columns c0 of Y) = sign * X[m x k] Z[k x n] for float matrices of row stride kLd; 4 columns of one
@@ -62,16 +64,17 @@ __device__ __forceinline__ void small_product(const float *X, const float *Z, in
 }
 
 template <typename T, int DKT>
-__global__ void __launch_bounds__(128, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : PrepSmem<T, DKT>::kBytes < 76000 ? 3 : 2)
+__global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : PrepSmem<T, DKT>::kBytes < 76000 ? 3 : 2)
     k_delta_prep(DeltaArgs a, unsigned char *ws, unsigned char *images, unsigned *flags) {
     using L = PrepSmem<T, DKT>;
     constexpr int NB = Parts<T>::n, kPart = 2 * kC * DKT * 2;
     extern __shared__ __align__(1024) unsigned char smem[];
     float *Ts = reinterpret_cast<float *>(smem), *As = reinterpret_cast<float *>(smem + L::kImg);
     unsigned char *parts = smem + kMat;
-    double *Gs = reinterpret_cast<double *>(smem + L::kBig);
+    // G / ln 2 as a float and what it leaves out: differences of large sums keep float's accuracy
+    float2 *Gs = reinterpret_cast<float2 *>(smem + L::kBig);
     float *cs = reinterpret_cast<float *>(Gs + kC), *bs = cs + kC;
-    uint64_t *bar = reinterpret_cast<uint64_t *>(bs + 2 * kC);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(bs + kC);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 1);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
@@ -93,15 +96,15 @@ __global__ void __launch_bounds__(128, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
     const int rows = sq.len - c0 < kC ? (int)(sq.len - c0) : kC;
     const long long tok = sq.tok0 + c0;
 
-    load_image<T, DKT>(smem, kPart, 2048, (const T *)a.k + tok * a.sk + (long long)hk * a.dk, a.sk, rows, a.dk, warp, 4);
+    load_image<T, DKT>(smem, kPart, 2048, (const T *)a.k + tok * a.sk + (long long)hk * a.dk, a.sk, rows, a.dk, warp, 8);
     load_image<T, DKT>(smem + 1024, kPart, 2048, (const T *)a.q + tok * a.sq + (long long)hk * a.dk, a.sq, rows, a.dk,
-                       warp, 4);
+                       warp, 8);
     if (warp == 0) umma::tmem_alloc(tslot, 128);
     if (tid == 0) {
         umma::mbar_init(bar, 1);
         umma::fence_mbar_init();
     }
-    if (warp == 1) {   // running sums of g in double: differences of large sums keep float's accuracy
+    if (warp == 1) {   // running sums of g, in units of ln 2, in double
         const int j = 2 * lane;
         const long long at = tok * a.hv + hv;
         float g0 = j < rows ? __ldg(a.g + at + (long long)j * a.hv) : 0.0f;
@@ -111,25 +114,28 @@ __global__ void __launch_bounds__(128, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
         // exp(-1e5) is 0 as exp(-inf) is, and differences stay numbers
         g0 = g0 < -1e5f ? -1e5f : g0;
         g1 = g1 < -1e5f ? -1e5f : g1;
-        double y = (double)g0 + (double)g1;
+        constexpr double kLog2e = 1.4426950408889634;   // 1 / ln 2
+        const double d1 = (double)g1 * kLog2e;
+        double y = (double)g0 * kLog2e + d1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double z = __shfl_up_sync(0xffffffffu, y, o);
             if (lane >= o) y += z;
         }
-        const double x = y - (double)g1;
-        Gs[j] = x;
-        Gs[j + 1] = y;
+        const double x = y - d1;
+        const float xf = (float)x, yf = (float)y;
+        Gs[j] = make_float2(xf, (float)(x - xf));
+        Gs[j + 1] = make_float2(yf, (float)(y - yf));
         bs[j] = b0;
         bs[j + 1] = b1;
         // beta_j e^(G at the end of j's 16 tokens - G_j); the factor e^(G_i - G at that end) is the row's
         const double end = __shfl_sync(0xffffffffu, y, lane | 7), all = __shfl_sync(0xffffffffu, y, 31);
-        cs[j] = b0 * expf((float)(end - x));
-        cs[j + 1] = b1 * expf((float)(end - y));
+        cs[j] = b0 * exp2f((float)(end - x));
+        cs[j + 1] = b1 * exp2f((float)(end - y));
         float *fac = reinterpret_cast<float *>(ws + (size_t)blockIdx.x * kUnitBytes + kTpBytes);
-        *reinterpret_cast<float2 *>(fac + j) = make_float2(expf((float)x), expf((float)y));
+        *reinterpret_cast<float2 *>(fac + j) = make_float2(exp2f(xf), exp2f(yf));
         *reinterpret_cast<float2 *>(fac + kC + j) =
-            make_float2(b0 * expf((float)(all - x)), b1 * expf((float)(all - y)));
+            make_float2(b0 * exp2f((float)(all - x)), b1 * exp2f((float)(all - y)));
     }
     umma::cp_async_wait_all();
     umma::fence_proxy_async();
@@ -158,47 +164,56 @@ __global__ void __launch_bounds__(128, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
         }
         __syncwarp();
     }
-    if (tid == 0 && hv % per == 0)   // the images for the chains; behind the first use of this memory for something else
-        bulk_store(images + (size_t)(slot * a.hk + hk) * kq_bytes<T, DKT>(), smem, kq_bytes<T, DKT>());
+    if (hv % per == 0) {   // the images for the chains (a bulk store would keep this memory busy for longer)
+        uint4 *dst = reinterpret_cast<uint4 *>(images + (size_t)(slot * a.hk + hk) * kq_bytes<T, DKT>());
+#pragma unroll 4
+        for (int n = tid; n < kq_bytes<T, DKT>() / 16; n += 256) dst[n] = reinterpret_cast<const uint4 *>(smem)[n];
+    }
     ok = umma::mbar_wait(bar, 0, kSpinLimit);
     umma::fence_after_sync();
-    const uint32_t mine = tm + ((uint32_t)(warp * 32) << 16);
-    const int i = tid & (kC - 1), ib = i >> 4;   // this thread's row of A (threads 0-63) or P, and its 16 tokens
-    const float mul = tid < kC ? 1.0f : a.scale;
+    const uint32_t mine = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const int i = tid & (kC - 1), ib = i >> 4;   // this thread's row, and its 16 tokens
+    const bool is_p = warp & 2;                  // of P, or of A
+    const int half = warp >> 2;                  // of the columns
+    const float mul = is_p ? a.scale : 1.0f;
     {
-        const double Gi = Gs[i];
+        const float2 Gi = Gs[i];
+        auto decay = [&](int j) {   // e^(G_i - G_j)
+            const float2 Gj = Gs[j];
+            return exp2f((Gi.x - Gj.x) + (Gi.y - Gj.y));
+        };
 #pragma unroll
-        for (int c = 0; c < kC; c += 16) {
+        for (int n = 0; n < 2; ++n) {
+            const int c = 32 * half + 16 * n;
             float d[16];
             tm_ld16(mine + c, d);
-            const int last = c + 15;
             if (c / 16 < ib) {   // all columns are earlier tokens: one factor for the row, one for each column
-                const float rf = mul * expf((float)(Gi - Gs[last]));
+                const float rf = mul * decay(c + 15);
+                float e[16];
+                get16(cs + c, e);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) d[j] *= rf * cs[c + j];
+                for (int j = 0; j < 16; ++j) d[j] *= rf * e[j];
             } else if (c / 16 == ib) {
-                const int m = tid < kC ? i : i + 1;
+                const int m = is_p ? i + 1 : i;
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    d[j] = c + j < m ? d[j] * (mul * bs[c + j]) * expf((float)(Gi - Gs[c + j])) : 0.0f;
+                for (int j = 0; j < 16; ++j) d[j] = c + j < m ? d[j] * (mul * bs[c + j]) * decay(c + j) : 0.0f;
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) d[j] = 0.0f;
             }
-            if (warp < 2) {
+            if (!is_p) {
 #pragma unroll
                 for (int j = 0; j < 16; j += 4)
                     *reinterpret_cast<float4 *>(As + i * kLd + c + j) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+            } else {   // P as operand; what its rows 0-63 hold only meets results that go unread
+                tm_split16(mine + c, mine + 64 + c / 2, d);
             }
-            // P as operand; rows 0-63 of it are A's and their products go unread
-            tm_split16(mine + c, mine + 64 + c / 2, d);
         }
         tm_wait_st();
     }
-    if (tid == 0) bulk_store_read();
     umma::fence_before_sync();
     __syncthreads();
-    {   // the 16 x 16 diagonal blocks of T by columns, a warp each: x_r = [r = c] - sum_{j < r} A_rj x_j
+    if (warp < 4) {   // the 16 x 16 diagonal blocks of T by columns, a warp each: x_r = [r = c] - sum_{j < r} A_rj x_j
         const int o = 16 * warp, c = lane & 15;
         float x[16];
 #pragma unroll
@@ -222,12 +237,12 @@ __global__ void __launch_bounds__(128, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
     // T21 = -T22 (A21 T11), first for the two pairs of 16 x 16 blocks, then for
     // the 32 x 32 ones; A21 T11 goes where A12 = 0 lies
     {
-        const int o = 32 * (warp >> 1), t = tid & 63;
-        small_product<16, 16, 16, false>(As + (o + 16) * kLd + o, Ts + o * kLd + o, t, 64, [&](int r, int c, float4 y) {
+        const int o = 32 * half, t = tid & 127;
+        small_product<16, 16, 16, false>(As + (o + 16) * kLd + o, Ts + o * kLd + o, t, 128, [&](int r, int c, float4 y) {
             *reinterpret_cast<float4 *>(As + (o + r) * kLd + o + 16 + c) = y;
         });
         __syncthreads();
-        small_product<16, 16, 16, true>(Ts + (o + 16) * kLd + o + 16, As + o * kLd + o + 16, t, 64,
+        small_product<16, 16, 16, true>(Ts + (o + 16) * kLd + o + 16, As + o * kLd + o + 16, t, 128,
                                         [&](int r, int c, float4 y) {
                                             *reinterpret_cast<float4 *>(Ts + (o + 16 + r) * kLd + o + c) = y;
                                             *reinterpret_cast<float4 *>(Ts + (o + r) * kLd + o + 16 + c) =
@@ -235,11 +250,11 @@ __global__ void __launch_bounds__(128, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
                                         });
     }
     __syncthreads();
-    small_product<32, 32, 32, false>(As + 32 * kLd, Ts, tid, 128, [&](int r, int c, float4 y) {
+    small_product<32, 32, 32, false>(As + 32 * kLd, Ts, tid, 256, [&](int r, int c, float4 y) {
         *reinterpret_cast<float4 *>(As + r * kLd + 32 + c) = y;
     });
     __syncthreads();
-    small_product<32, 32, 32, true>(Ts + 32 * kLd + 32, As + 32, tid, 128, [&](int r, int c, float4 y) {
+    small_product<32, 32, 32, true>(Ts + 32 * kLd + 32, As + 32, tid, 256, [&](int r, int c, float4 y) {
         *reinterpret_cast<float4 *>(Ts + (32 + r) * kLd + c) = y;
     });
     __syncthreads();
@@ -247,8 +262,8 @@ __global__ void __launch_bounds__(128, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
     {   // T's parts: into shared memory as operand and to the workspace
         const int r = tid & 63;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int cg = (tid >> 6) + 2 * n;
+        for (int n = 0; n < 2; ++n) {
+            const int cg = (tid >> 6) + 4 * n;
             uint32_t w[4][3];
             const bool in = cg <= r / 8;   // the lower triangle; columns behind the diagonal's block are not read above it
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
@@ -279,7 +294,7 @@ __global__ void __launch_bounds__(128, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
     // PT = P T, K over T's rows, 32 columns at a time (rows 32 and up for the
     // second half), so that P's parts and the result share 128 columns
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int pass = 0; pass < 2; ++pass) {
         umma::fence_before_sync();
         __syncthreads();
         umma::fence_after_sync();
@@ -291,9 +306,9 @@ __global__ void __launch_bounds__(128, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
 #pragma unroll
                     for (int p = 0; p <= o; ++p)
 #pragma unroll
-                        for (int ks = 2 * half; ks < kC / 16; ++ks) {
+                        for (int ks = 2 * pass; ks < kC / 16; ++ks) {
                             mma_ts(tm + 96, tm + (p < 2 ? 16 * ks + 8 * p : 64 + 8 * ks),
-                                   desc_mn(saddr(parts) + (o - p) * kTImg + ks * 256 + half * 4096, 128, 1024),
+                                   desc_mn(saddr(parts) + (o - p) * kTImg + ks * 256 + pass * 4096, 128, 1024),
                                    idesc(32, false, true), acc);
                             acc = true;
                         }
@@ -301,30 +316,26 @@ __global__ void __launch_bounds__(128, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
             }
             __syncwarp();
         }
-        ok = umma::mbar_wait(bar, 1 ^ half, kSpinLimit) && ok;
+        ok = umma::mbar_wait(bar, 1 ^ pass, kSpinLimit) && ok;
         umma::fence_after_sync();
-        if (warp >= 2) {
+        if (is_p) {
+            float d[16];
+            tm_ld16(mine + 96 + 16 * half, d);
+            const int c = 32 * pass + 16 * half;
+            if (ib >= c / 16)
 #pragma unroll
-            for (int c = 0; c < 32; c += 16) {
-                float d[16];
-                tm_ld16(mine + 96 + c, d);
-                const int cc = 32 * half + c;
-                if (ib >= cc / 16)
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[4][3];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[4][3];
+                    for (int j = 0; j < 4; ++j) split<3>(d[8 * h + 2 * j], d[8 * h + 2 * j + 1], w[j]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) split<3>(d[8 * h + 2 * j], d[8 * h + 2 * j + 1], w[j]);
-#pragma unroll
-                        for (int q = 0; q < 3; ++q)
-                            *reinterpret_cast<uint4 *>(out + q * kTpImage + packed(i, cc / 8 + h, 1)) =
-                                make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
-                    }
-            }
+                    for (int q = 0; q < 3; ++q)
+                        *reinterpret_cast<uint4 *>(out + q * kTpImage + packed(i, c / 8 + h, 1)) =
+                            make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+                }
         }
     }
     if (!ok && flags && tid == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
-    if (tid == 0) bulk_store_wait();
     umma::fence_before_sync();
     __syncthreads();
     if (warp == 0) umma::tmem_dealloc(tm, 128);
@@ -336,7 +347,7 @@ cudaError_t run(const DeltaArgs &a, void *ws, unsigned *flags, cudaStream_t st) 
     cudaError_t e = cudaFuncSetAttribute(k_delta_prep<T, DKT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const long long units = slots(a.tokens, a.n) * a.hv;
-    k_delta_prep<T, DKT><<<(unsigned)units, 128, smem, st>>>(a, (unsigned char *)ws,
+    k_delta_prep<T, DKT><<<(unsigned)units, 256, smem, st>>>(a, (unsigned char *)ws,
                                                              (unsigned char *)ws + (size_t)units * kUnitBytes, flags);
     return cudaGetLastError();
 }

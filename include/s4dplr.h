@@ -677,6 +677,27 @@ s4_status s4_gated_delta_forward(s4_dtype dtype, const void *q, long long q_stri
                                  void *o, float *final_state, int keep, void *workspace, size_t workspace_bytes,
                                  unsigned *d_flags, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * s4_gated_delta_backward -- the gradients of s4_gated_delta_forward for d_o
+ * [like o, contiguous] and d_final_state ([Bt, Hv, Dk, Dv] float; NULL: zero).
+ * workspace: that of a forward call with keep != 0 for the same inputs, sizes,
+ * cu_seqlens and scale, which ran before on the same stream (or is waited
+ * for); it is not used up, but written to: two backward passes of one forward
+ * pass may not run at the same time. g and beta as given there (q, k and v are
+ * read from the workspace).
+ *   dq, dk [like contiguous q, k], dv [like o] of the element type; dg, dbeta
+ *   [like g] float; d_initial_state [Bt, Hv, Dk, Dv] float (NULL: not wanted;
+ *   may be d_final_state). Gradients of a key head are summed over its value
+ *   heads in order: the same inputs give the same bits. Rows outside all
+ *   sequences are left as they were.
+ * Errors as s4_gated_delta_forward.
+ * ------------------------------------------------------------------------ */
+s4_status s4_gated_delta_backward(s4_dtype dtype, const float *g, const float *beta, float scale,
+                                  const int *cu_seqlens, int Bt, long long tokens, int Hk, int Hv, int Dk, int Dv,
+                                  const void *d_o, const float *d_final_state, void *dq, void *dk, void *dv,
+                                  float *dg, float *dbeta, float *d_initial_state, void *workspace,
+                                  size_t workspace_bytes, unsigned *d_flags, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,6 +29,7 @@ __all__ = [
     "kernel_dplr_backward", "kernel_dplr_backward_workspace_size", "s4d_kernel_vandermonde_backward", "load",
     "layernorm", "layernorm_backward", "layernorm_backward_workspace_size", "layernorm_channels_backward",
     "gated_delta_step", "gated_delta_scan", "gated_delta_workspace_size", "gated_delta_forward",
+    "gated_delta_backward",
 ]
 
 
@@ -790,3 +791,28 @@ def gated_delta_forward(q, k, v, g, beta, *, scale=None, initial_state=None, cu_
               float(scale), _ptr(initial_state), _ptr(cu_seqlens), n, Bt * T, Hk, Hv, Dk, Dv, _ptr(out),
               _ptr(final_state), int(bool(keep)), _ptr(workspace), workspace.numel(), _flags_ptr(flags), _stream())
     return out, final_state, workspace
+
+
+def gated_delta_backward(q, k, v, g, beta, do, workspace, *, scale=None, dfinal_state=None, cu_seqlens=None,
+                         flags=None):
+    """Gradients of gated_delta_forward (s4_gated_delta_backward): do like o,
+    dfinal_state [N, Hv, Dk, Dv] (zeros by default), workspace the one that
+    gated_delta_forward(..., keep=True) of the same inputs returned. Returns
+    dict(q, k, v of their type, contiguous; g, beta, initial_state float32)."""
+    kind, _, (Bt, T, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
+    n, dev = _sequences(cu_seqlens, Bt), v.device
+    _buffer(_cuda(do, "do"), "do", v.shape, v.dtype, dev)
+    if dfinal_state is not None:
+        _buffer(_cuda(dfinal_state, "dfinal_state"), "dfinal_state", (n, Hv, Dk, Dv), torch.float32, dev)
+    _cuda(workspace, "workspace", torch.uint8)
+    # rows that no packed sequence covers get no gradient
+    new = torch.empty if cu_seqlens is None else torch.zeros
+    out = {"q": new(q.shape, dtype=q.dtype, device=dev), "k": new(k.shape, dtype=k.dtype, device=dev),
+           "v": new(v.shape, dtype=v.dtype, device=dev), "g": new(g.shape, dtype=g.dtype, device=dev),
+           "beta": new(g.shape, dtype=g.dtype, device=dev),
+           "initial_state": torch.empty(n, Hv, Dk, Dv, dtype=torch.float32, device=dev)}
+    scale = Dk ** -0.5 if scale is None else scale
+    _lib.call("s4_gated_delta_backward", kind, _ptr(g), _ptr(beta), float(scale), _ptr(cu_seqlens), n, Bt * T, Hk, Hv,
+              Dk, Dv, _ptr(do), _ptr(dfinal_state), *(_ptr(out[m]) for m in ("q", "k", "v", "g", "beta", "initial_state")),
+              _ptr(workspace), workspace.numel(), _flags_ptr(flags), _stream())
+    return out

@@ -72,6 +72,8 @@ SIGNATURES = {
     "s4_gated_delta_workspace_size": (_i, [_i, _i, _ll, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     "s4_gated_delta_forward": (_i, [_i, _p, _ll, _p, _ll, _p, _ll, _p, _p, _f, _p, _p, _i, _ll, _i, _i, _i, _i, _p, _p,
                                     _i, _p, _sz, _p, _p]),
+    "s4_gated_delta_backward": (_i, [_i, _p, _p, _f, _p, _i, _ll, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p,
+                                     _sz, _p, _p]),
 }
 
 _lib = None

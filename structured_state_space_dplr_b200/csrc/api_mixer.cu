@@ -240,4 +240,48 @@ s4_status s4_gated_delta_forward(s4_dtype dtype, const void *q, long long q_stri
         s4::launch_delta_forward(dtype, a, initial_state, final_state, workspace, ks, ke, d_flags, stream));
 }
 
+s4_status s4_gated_delta_backward(s4_dtype dtype, const float *g, const float *beta, float scale,
+                                  const int *cu_seqlens, int Bt, long long tokens, int Hk, int Hv, int Dk, int Dv,
+                                  const void *d_o, const float *d_final_state, void *dq, void *dk, void *dv,
+                                  float *dg, float *dbeta, float *d_initial_state, void *workspace,
+                                  size_t workspace_bytes, unsigned *d_flags, cudaStream_t stream) {
+    s4_status s = chunk_sizes(dtype, cu_seqlens != nullptr, Bt, tokens, Hk, Hv, Dk, Dv);
+    if (s != S4_OK) return s;
+    if (!std::isfinite(scale)) return S4_ERR_INVALID_ARG;
+    if (tokens > 0 && any_null({g, beta, d_o, dq, dk, dv, dg, dbeta})) return S4_ERR_INVALID_ARG;
+    if (!aligned(16, {d_o, dq, dk, dv, d_final_state, d_initial_state}) ||
+        !aligned(4, {g, beta, dg, dbeta, cu_seqlens, d_flags}))
+        return S4_ERR_INVALID_ARG;
+    const DeltaWork w = delta_work(dtype, Bt, tokens, Hk, Hv, Dk, Dv, 1);
+    if (!workspace || !aligned(256, {workspace}) || workspace_bytes < w.total) return S4_ERR_WORKSPACE;
+    const double tok = (double)tokens, gate = tok * Hv * 4.0, st = 4.0 * Bt * Hv * Dk * Dv;
+    const double nk = tok * Hk * Dk * dtype_size(dtype), nv = tok * Hv * Dv * dtype_size(dtype);
+    // d_initial_state may be d_final_state: a state is read before it is written
+    if (overlapping({{g, gate, false},
+                     {beta, gate, false},
+                     {cu_seqlens, 4.0 * (Bt + 1.0), false},
+                     {d_o, nv, false},
+                     {d_final_state == d_initial_state ? nullptr : d_final_state, st, false},
+                     {dq, nk, true},
+                     {dk, nk, true},
+                     {dv, nv, true},
+                     {dg, gate, true},
+                     {dbeta, gate, true},
+                     {d_initial_state, st, true},
+                     {d_flags, 4.0, true},
+                     {workspace, (double)workspace_bytes, true}}))
+        return S4_ERR_INVALID_ARG;
+    s4::DeltaArgs a{};
+    a.g = g, a.beta = beta, a.n = Bt, a.hk = Hk, a.hv = Hv, a.dk = Dk, a.dv = Dv, a.scale = scale;
+    a.cu = cu_seqlens, a.t = cu_seqlens ? 0 : (int)(tokens / Bt), a.tokens = tokens;
+    char *p = (char *)workspace + w.prep;
+    float *ks = (float *)p, *ke = (float *)(p + w.state), *kds = (float *)(p + w.state + w.rows),
+          *kdr = (float *)(p + 2 * w.state + w.rows);
+    s = cuda_status(s4::launch_delta_backward(dtype, a, d_o, d_final_state, d_initial_state, workspace, dv, kds, kdr,
+                                              d_flags, stream));
+    if (s != S4_OK || tokens == 0) return s;
+    return cuda_status(
+        s4::launch_delta_gradient(dtype, a, d_o, workspace, ks, ke, kds, kdr, dq, dk, dg, dbeta, d_flags, stream));
+}
+
 }  // extern "C"

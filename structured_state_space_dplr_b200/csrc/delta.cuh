@@ -72,6 +72,61 @@ __device__ __forceinline__ Seq sequence(const DeltaArgs &a, int s) {
     r.slot0 = r.tok0 / kC + s;
     return r;
 }
+// the chunk that owns a slot: its first token and its tokens (0: none)
+struct Chunk {
+    long long tok;
+    int rows;
+};
+__device__ __forceinline__ Chunk chunk_of(const DeltaArgs &a, long long slot) {
+    int s = 0;   // the last sequence that starts at or before the slot
+    for (int lo = 0, hi = a.n; lo < hi;) {
+        const int m = (lo + hi) >> 1;
+        if (sequence(a, m).slot0 <= slot) {
+            s = m;
+            lo = m + 1;
+        } else {
+            hi = m;
+        }
+    }
+    const Seq sq = sequence(a, s);
+    const long long c0 = (slot - sq.slot0) * kC;
+    Chunk c;
+    c.tok = sq.tok0 + c0;
+    c.rows = c0 < 0 || c0 >= sq.len ? 0 : sq.len - c0 < kC ? (int)(sq.len - c0) : kC;
+    return c;
+}
+
+// Running sums of g over the chunk, in units of ln 2 and in double (differences
+// of large sums keep float's accuracy), by one warp: lane l has the tokens 2 l
+// (x, b0 = its beta) and 2 l + 1 (y, b1); tokens past `rows` have g = beta = 0.
+struct GateSums {
+    double x, y;
+    float b0, b1;
+};
+__device__ __forceinline__ GateSums gate_sums(const DeltaArgs &a, long long tok, int hv, int rows, int lane) {
+    const int j = 2 * lane;
+    const long long at = tok * a.hv + hv;
+    float g0 = j < rows ? __ldg(a.g + at + (long long)j * a.hv) : 0.0f;
+    float g1 = j + 1 < rows ? __ldg(a.g + at + (long long)(j + 1) * a.hv) : 0.0f;
+    GateSums r;
+    r.b0 = j < rows ? __ldg(a.beta + at + (long long)j * a.hv) : 0.0f;
+    r.b1 = j + 1 < rows ? __ldg(a.beta + at + (long long)(j + 1) * a.hv) : 0.0f;
+    // exp(-1e5) is 0 as exp(-inf) is, and differences stay numbers
+    g0 = g0 < -1e5f ? -1e5f : g0;
+    g1 = g1 < -1e5f ? -1e5f : g1;
+    constexpr double kLog2e = 1.4426950408889634;   // 1 / ln 2
+    const double d1 = (double)g1 * kLog2e;
+    double y = (double)g0 * kLog2e + d1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+    }
+    r.x = y - d1;
+    r.y = y;
+    return r;
+}
+
 __host__ __device__ inline long long slots(long long tokens, int n) { return tokens / kC + n; }
 
 // ---------------------------------------------------------------- split ----
@@ -189,22 +244,25 @@ __device__ __forceinline__ void get16(const float *p, float (&v)[16]) {
     }
 }
 
-// 16 floats (consecutive K elements of a lane, one K step) as three parts of
+// 16 floats (consecutive K elements of a lane, one K step) as N parts of
 // 8 columns: the high and middle ones side by side at `at`, which is where an
 // accumulator of the same 16 columns lies, the low one at `lo`
-__device__ __forceinline__ void tm_split16(uint32_t at, uint32_t lo, const float (&v)[16]) {
-    uint32_t p[3][8];
+template <int N>
+__device__ __forceinline__ void tm_parts16(uint32_t at, uint32_t lo, const float (&v)[16]) {
+    uint32_t p[N][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        uint32_t s[3];
-        split<3>(v[2 * i], v[2 * i + 1], s);
-        p[0][i] = s[0];
-        p[1][i] = s[1];
-        p[2][i] = s[2];
+        uint32_t s[N];
+        split<N>(v[2 * i], v[2 * i + 1], s);
+#pragma unroll
+        for (int j = 0; j < N; ++j) p[j][i] = s[j];
     }
     tm_st8(at, p[0]);
-    tm_st8(at + 8, p[1]);
-    tm_st8(lo, p[2]);
+    if constexpr (N > 1) tm_st8(at + 8, p[1]);
+    if constexpr (N > 2) tm_st8(lo, p[2]);
+}
+__device__ __forceinline__ void tm_split16(uint32_t at, uint32_t lo, const float (&v)[16]) {
+    tm_parts16<3>(at, lo, v);
 }
 
 // 16 bytes to shared memory, zeros where `in` is false
@@ -300,6 +358,109 @@ __device__ __forceinline__ V uniform(V v) { return __shfl_sync(0xffffffffu, v, 0
 // the workspace: units of (slot, value head), then the images of [K; Q] of (slot, key head)
 template <typename T, int DKT>
 __host__ __device__ constexpr int kq_bytes() { return Parts<T>::n * 2 * kC * DKT * 2; }
+
+// ----------------------------------------------------- the two chains ----
+// warps 0-7: element-wise steps; 8: products; 9-11: loads
+constexpr int kEpiWarps = 8, kLoadWarps = 3, kThreads = (kEpiWarps + 1 + kLoadWarps) * 32;
+
+// parts of [K; Q], 128 rows; then T and PT and factors, V as it is
+template <typename T, int DKT>
+struct Stage {
+    static constexpr int NB = Parts<T>::n;
+    static constexpr int kImg = 2 * kC * DKT * 2, kTp = NB * kImg, kV = kTp + kUnitBytes;
+    static __host__ __device__ int bytes(int dv) { return kV + kC * dv * (int)sizeof(T); }
+    static __host__ __device__ int count(int dv) { return 2 * bytes(dv) + 256 <= 232448 ? 2 : 1; }
+};
+
+// One chunk's stage, by the loading threads (lt): images and unit as they lie
+// in the workspace, and 64 rows of V or dO; full when m has kLoadWarps * 32 + 1
+// arrivals and the copies' bytes.
+template <typename T, int DKT>
+__device__ __forceinline__ void load_stage(unsigned char *sp, const unsigned char *image, const unsigned char *unit,
+                                           const T *rows, long long stride, int left, int dv, int lt, uint64_t *m) {
+    using L = Stage<T, DKT>;
+    if (lt == 0) {
+        mbar_expect(m, kUnitBytes + L::kTp);
+        bulk_load(sp, image, L::kTp, m);
+        bulk_load(sp + L::kTp, unit, kUnitBytes, m);
+        mbar_arrive(m);
+    }
+    load_rows<T>(sp + L::kV, rows, stride, left < kC ? left : kC, dv, lt, kLoadWarps * 32, m);
+}
+// the same on its way to L2
+template <typename T, int DKT>
+__device__ __forceinline__ void prefetch_stage(const unsigned char *image, const unsigned char *unit, const T *rows,
+                                               long long stride, int left, int dv, int lt) {
+    if (lt < kC && lt < left) {
+        const char *p = (const char *)(rows + lt * stride);
+        for (int i = 0; i < dv * (int)sizeof(T); i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+    }
+    if (lt == kC) {
+        bulk_prefetch(unit, kUnitBytes);
+        bulk_prefetch(image, Stage<T, DKT>::kTp);
+    }
+}
+
+// 16 tokens of this lane's channel to o, `row` elements apart, the first n of
+// them. 16-bit types: neighbouring lanes swap so that each stores two channels
+// of every other token in one word (dv is even: both channels are there or not).
+template <typename T>
+__device__ __forceinline__ void store16(T *o, long long row, const float (&x)[16], int lane, bool vin, int n) {
+    if constexpr (sizeof(T) == 4) {
+        if (vin) {
+            if (n >= 16) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j * row] = x[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (j < n) o[j * row] = x[j];
+            }
+        }
+    } else {
+        const bool odd = lane & 1;
+        Pack<T, 2> w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? x[2 * j] : x[2 * j + 1], 1);
+            w[j].v[0] = from_f<T>(odd ? other : x[2 * j]);
+            w[j].v[1] = from_f<T>(odd ? x[2 * j + 1] : other);
+        }
+        if (odd) {   // the odd lane has the second token of each pair
+            o += row - 1;
+            --n;
+        }
+        if (vin) {
+            if (n >= 15) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) *reinterpret_cast<Pack<T, 2> *>(o + 2 * j * row) = w[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (2 * j < n) *reinterpret_cast<Pack<T, 2> *>(o + 2 * j * row) = w[j];
+            }
+        }
+    }
+}
+
+// What the gradient kernel reads lies in groups of 8 consecutive elements of
+// one row, the rows of a group side by side: states as [dk / 8][dv][8] (a lane
+// of the chains, one v, stores 8 of its dk), E and dR as [dv / 8][64][8].
+template <int HC>
+__device__ __forceinline__ void store_state(float *p, const float (&S)[HC], int h, int v, int dk, int dv) {
+#pragma unroll
+    for (int i = 0; i < HC; i += 8)
+        if (h * HC + i < dk) {
+            float4 *q = reinterpret_cast<float4 *>(p + ((size_t)((h * HC + i) / 8) * dv + v) * 8);
+            q[0] = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+            q[1] = make_float4(S[i + 4], S[i + 5], S[i + 6], S[i + 7]);
+        }
+}
+__device__ __forceinline__ void store_tokens(float *p, const float (&x)[16], int j0, int v) {
+    p += ((v >> 3) * kC + j0) * 8 + (v & 7);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) p[8 * j] = x[j];
+}
 
 }  // namespace delta
 }  // namespace s4

@@ -1,0 +1,351 @@
+// delta_back.cu -- the chunked gated delta rule, backward in the states: one
+// block walks the chunks of one sequence and value head from the last to the
+// first with the state's gradient in registers.
+//
+// With dS1 the gradient of the state behind a chunk (transposed like the
+// forward chain, value channel = tensor-memory lane):
+//     D1 = dS1^T K^T                                         (128 x 64)
+//     dR^T = (beta e^(G_C - G) D1) T + dO^T PT               (128 x 64)
+//     dS0^T = e^(G_C) dS1^T + (scale e^G dO)^T Q - (e^G dR)^T K   (128 x Dk)
+// dR is the gradient of V and, with dS1, what the gradient kernel needs. The
+// products with dO do not depend on the chain and fill its gaps. T and PT are
+// read by columns (MN-major) from the forward's images, 16 columns a product.
+// Roles and bounds as in the forward chain.
+#include "delta.cuh"
+#include "s4dplr.h"
+
+namespace s4 {
+namespace {
+
+using namespace delta;
+
+// Tensor-memory columns; parts in the place of the accumulator they come from
+// (16 columns by 16 columns), their low ones apart:
+//   kTmS   the state gradient's parts (128), D3 in their place, low kTmSl
+//   kTmK   dS1^T K^T (64), then the parts of its scaled value, low kTmKl
+//   kTmR   dR^T (64), then the parts of -e^G dR, low kTmRl
+//   kTmX   the parts of dO (64 columns), low kTmXl; later those of scale e^G dO
+constexpr int kTmS = 0, kTmSl = 128, kTmK = 192, kTmR = 256, kTmX = 320, kTmKl = 384, kTmRl = 416, kTmXl = 448;
+
+enum { bFull = 0, bEmpty = 2, bS = 4, bK = 8, bR = 10, bX = 12, bY, bM1, bMx, bM2, bM3, bCount };
+
+template <typename T, int DKT>
+__global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, const T *dout, const float *dlast,
+                                                                float *dinit, const unsigned char *ws,
+                                                                const unsigned char *images, T *dv, float *keep_ds,
+                                                                float *keep_dr, unsigned *flags) {
+    using L = Stage<T, DKT>;
+    constexpr int NB = Parts<T>::n, HC = DKT / 2, NS = DKT / 32;   // NS: K steps of a half of the state
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const int ST = L::count(a.dv), stage_bytes = L::bytes(a.dv);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + ST * stage_bytes);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + bCount);
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    const int hv = blockIdx.x % a.hv, s = blockIdx.x / a.hv, hk = hv / (a.hv / a.hk);
+    const Seq sq = sequence(a, s);
+    const int chunks = uniform((sq.len + kC - 1) / kC);
+    const long long orow = (long long)a.hv * a.dv;   // dO and dV are contiguous
+
+    if (warp == 0) umma::tmem_alloc(tslot, 512);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            umma::mbar_init(bars + bFull + i, kLoadWarps * 32 + 1);
+            umma::mbar_init(bars + bEmpty + i, 1 + kEpiWarps);
+        }
+        for (int i = bS; i <= bY; ++i) umma::mbar_init(bars + i, kEpiWarps);
+        for (int i = bM1; i <= bM3; ++i) umma::mbar_init(bars + i, 1);
+        umma::fence_mbar_init();
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tm = uniform(*tslot);
+    bool ok = true;
+
+    if (warp > kEpiWarps) {
+        // ------------------------------------------------------ loading ----
+        const int lt = tid - (kEpiWarps + 1) * 32;
+        for (int n = 0, st = 0, turn = 0; n < chunks; ++n) {
+            const int c = chunks - 1 - n;
+            const long long slot = sq.slot0 + c;
+            const unsigned char *up = ws + (size_t)(slot * a.hv + hv) * kUnitBytes;
+            const unsigned char *ip = images + (size_t)(slot * a.hk + hk) * L::kTp;
+            const T *op = dout + (sq.tok0 + (long long)c * kC) * orow + (long long)hv * a.dv;
+            if (c > 0)
+                prefetch_stage<T, DKT>(ip - (size_t)a.hk * L::kTp, up - (size_t)a.hv * kUnitBytes, op - kC * orow, orow,
+                                       kC, a.dv, lt);
+            ok = umma::mbar_wait(bars + bEmpty + st, (turn & 1) ^ 1, kSpinLimit);   // the first use needs no wait
+            if (!ok) break;
+            load_stage<T, DKT>(smem + st * stage_bytes, ip, up, op, orow, sq.len - c * kC, a.dv, lt, bars + bFull + st);
+            if (++st == ST) {
+                st = 0;
+                ++turn;
+            }
+        }
+        // every copy has been waited for by the readers, unless a wait ran out: then here
+        if (!ok)
+            for (int i = 0; i < ST; ++i) umma::mbar_wait(bars + bFull + i, 0, 1u << 16);
+    } else if (warp == kEpiWarps) {
+        // ----------------------------------------------------- products ----
+        const uint32_t base = saddr(smem);
+        for (int n = 0, st = 0, turn = 0; n < chunks && ok; ++n) {
+            const int pn = n & 1;
+            const uint32_t k0 = base + st * stage_bytes, t0 = k0 + L::kTp;
+            // columns 16 ks of dR^T (+)= part p of operand (at, low), K step ib, times part j of T (pt = 0) or PT (1)
+            auto t_times = [&](uint32_t at, uint32_t low, int p, int ib, int j, int pt, int ks, bool acc) {
+                mma_ts(tm + kTmR + 16 * ks, tm + (p < 2 ? at + 16 * ib + 8 * p : low + 8 * ib),
+                       desc_mn(t0 + j * kTpImage + tp_offset(ks) + pt * tp_rows(ks) + (ib - ks) * 256, 128,
+                               tp_group(ks)),
+                       idesc(16, false, true), acc);
+            };
+            ok = umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit);
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {   // D1 = dS1^T K^T, steps m and NS + m
+                ok = ok && umma::mbar_wait(bars + bS + m, pn, kSpinLimit);
+                umma::fence_after_sync();
+                if (ok && elect()) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int o = 2; o >= 0; --o)
+#pragma unroll
+                            for (int j = 0; j < NB; ++j) {
+                                if (o - j < 0) continue;
+                                const int ks = h * NS + m, p = o - j;
+                                mma_ts(tm + kTmK, tm + (p < 2 ? kTmS + 16 * ks + 8 * p : kTmSl + 8 * ks),
+                                       desc_k(k0 + j * L::kImg + ks * 4096, 2048, 128), idesc(kC, false, false),
+                                       m + h > 0 || o < 2 || j > 0);
+                            }
+                    if (m == NS - 1) umma::commit(bars + bM1);
+                }
+                __syncwarp();
+            }
+            // dR^T = dO^T PT + ..
+            ok = ok && umma::mbar_wait(bars + bX, pn, kSpinLimit);
+            umma::fence_after_sync();
+            if (ok && elect()) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                    for (int ib = 3; ib >= ks; --ib)
+#pragma unroll
+                        for (int o = 2; o >= 0; --o)
+#pragma unroll
+                            for (int p = 0; p < NB; ++p)
+                                if (o - p >= 0) t_times(kTmX, kTmXl, p, ib, o - p, 1, ks, ib < 3 || o < 2 || p > 0);
+                umma::commit(bars + bMx);
+            }
+            __syncwarp();
+            // .. + (beta e^(G_C - G) D1) T
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                ok = ok && umma::mbar_wait(bars + bK + m, pn, kSpinLimit);
+                umma::fence_after_sync();
+                if (ok && elect()) {
+#pragma unroll
+                    for (int ib = m; ib < 4; ib += 2)
+#pragma unroll
+                        for (int ks = 0; ks <= ib; ++ks)
+#pragma unroll
+                            for (int o = 2; o >= 0; --o)
+#pragma unroll
+                                for (int p = 0; p <= o; ++p) t_times(kTmK, kTmKl, p, ib, o - p, 0, ks, true);
+                    if (m == 1) umma::commit(bars + bM2);
+                }
+                __syncwarp();
+            }
+            // D3 = (scale e^G dO)^T Q - (e^G dR)^T K, in the place of the state gradient's parts
+            auto tok_times = [&](uint32_t at, uint32_t low, int row0, int ks, bool first) {
+#pragma unroll
+                for (int o = 2; o >= 0; --o)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        if (o - j < 0) continue;
+                        const int p = o - j;
+                        mma_ts(tm + kTmS, tm + (p < 2 ? at + 16 * ks + 8 * p : low + 8 * ks),
+                               desc_mn(k0 + j * L::kImg + row0 * 16 + ks * 256, 128, 2048), idesc(DKT, false, true),
+                               !first || o < 2 || j > 0);
+                    }
+            };
+            ok = ok && umma::mbar_wait(bars + bY, pn, kSpinLimit) && umma::mbar_wait(bars + bM1, pn, kSpinLimit);
+            umma::fence_after_sync();
+            if (ok && elect())
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) tok_times(kTmX, kTmXl, kC, ks, ks == 0);
+            __syncwarp();
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                ok = ok && umma::mbar_wait(bars + bR + m, pn, kSpinLimit);
+                umma::fence_after_sync();
+                if (ok && elect()) {
+                    tok_times(kTmR, kTmRl, 0, m, false);
+                    tok_times(kTmR, kTmRl, 0, 2 + m, false);
+                    if (m == 1) {
+                        umma::commit(bars + bM3);
+                        umma::commit(bars + bEmpty + st);
+                    }
+                }
+                __syncwarp();
+            }
+            if (++st == ST) {
+                st = 0;
+                ++turn;
+            }
+        }
+    } else {
+        // ------------------------------------------------- element-wise ----
+        const int h = warp >> 2, v = (warp & 3) * 32 + lane;   // half of the columns, value channel
+        const uint32_t mine = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        const bool vin = v < a.dv;
+        float S[HC];
+        const size_t st0 = ((size_t)s * a.hv + hv) * a.dk * a.dv + v;
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+            const int d = h * HC + i;
+            S[i] = dlast && vin && d < a.dk ? __ldg(dlast + st0 + (size_t)d * a.dv) : 0.0f;
+        }
+        auto done = [&](int bar) {   // this warp's tensor-memory writes (and reads) before the barrier
+            tm_wait_st();
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + bar);
+        };
+        for (int n = 0, st = 0, turn = 0; n < chunks; ++n) {
+            const int pn = n & 1, c = chunks - 1 - n, rows = sq.len - c * kC;
+            const unsigned char *sp = smem + st * stage_bytes;
+            const float *eg = reinterpret_cast<const float *>(sp + L::kTp + kTpBytes);
+            // lanes past dv compute what channel 0 would be; nothing of it is stored
+            const T *os = reinterpret_cast<const T *>(sp + L::kV) + (vin ? v : 0);
+            const long long unit = (sq.slot0 + c) * a.hv + hv;
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = S[16 * m + j];
+                tm_split16(mine + kTmS + 16 * (h * NS + m), mine + kTmSl + 8 * (h * NS + m), x);
+                done(bS + m);
+            }
+            if (vin) store_state<HC>(keep_ds + (size_t)unit * a.dk * a.dv, S, h, v, a.dk, a.dv);
+            ok = umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit);
+            if (!ok) break;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {   // dO^T
+                const int j0 = h * (kC / 2) + 16 * m;
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = to_f(os[(j0 + j) * a.dv]);
+                tm_parts16<NB>(mine + kTmX + j0, mine + kTmXl + j0 / 2, x);
+            }
+            done(bX);
+            ok = umma::mbar_wait(bars + bM1, pn, kSpinLimit);
+            if (!ok) break;
+            umma::fence_after_sync();
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {   // beta e^(G_C - G) D1
+                const int j0 = h * (kC / 2) + 16 * m;
+                float x[16], e[16];
+                get16(eg + kC + j0, e);
+                tm_ld16(mine + kTmK + j0, x);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] *= e[j];
+                tm_split16(mine + kTmK + j0, mine + kTmKl + j0 / 2, x);
+                done(bK + m);
+            }
+            ok = umma::mbar_wait(bars + bMx, pn, kSpinLimit);
+            if (!ok) break;
+            umma::fence_after_sync();
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {   // scale e^G dO^T, in the place of dO^T
+                const int j0 = h * (kC / 2) + 16 * m;
+                float x[16], e[16];
+                get16(eg + j0, e);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = to_f(os[(j0 + j) * a.dv]) * (a.scale * e[j]);
+                tm_split16(mine + kTmX + j0, mine + kTmXl + j0 / 2, x);
+            }
+            done(bY);
+            ok = umma::mbar_wait(bars + bM2, pn, kSpinLimit);
+            if (!ok) break;
+            umma::fence_after_sync();
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {   // dR^T = dV^T, and -e^G dR as the next operand
+                const int j0 = h * (kC / 2) + 16 * m;
+                float x[16], e[16];
+                get16(eg + j0, e);
+                tm_ld16(mine + kTmR + j0, x);
+                float y[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = -e[j] * x[j];
+                tm_split16(mine + kTmR + j0, mine + kTmRl + j0 / 2, y);
+                done(bR + m);
+                if (vin) store_tokens(keep_dr + (size_t)unit * kC * a.dv, x, j0, v);
+                store16<T>(dv + (sq.tok0 + (long long)c * kC + j0) * orow + (long long)hv * a.dv + v, orow, x, lane, vin,
+                           rows - j0);
+            }
+            const float total = eg[kC - 1];   // e^(G_C): rows past the end have g = 0
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + bEmpty + st);
+            ok = umma::mbar_wait(bars + bM3, pn, kSpinLimit);
+            if (!ok) break;
+            umma::fence_after_sync();
+#pragma unroll
+            for (int i = 0; i < HC; i += 16) {
+                float x[16];
+                tm_ld16(mine + kTmS + h * HC + i, x);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) S[i + j] = fmaf(total, S[i + j], x[j]);
+            }
+            if (++st == ST) {
+                st = 0;
+                ++turn;
+            }
+        }
+        if (dinit && vin) {
+#pragma unroll
+            for (int i = 0; i < HC; ++i)
+                if (h * HC + i < a.dk) dinit[st0 + (size_t)(h * HC + i) * a.dv] = S[i];
+        }
+    }
+    if (!ok && flags && lane == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
+    if (warp == kEpiWarps && !ok) {   // a wait that ran out may leave products in flight
+        if (lane == 0) umma::commit(bars + bM3);
+        __syncwarp();
+        umma::mbar_wait(bars + bM3, 0, 1u << 16);
+        umma::mbar_wait(bars + bM3, 1, 1u << 16);
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    if (warp == 0) umma::tmem_dealloc(tm, 512);
+}
+
+template <typename T, int DKT>
+cudaError_t run(const DeltaArgs &a, const void *dout, const float *dlast, float *dinit, const void *ws, void *dv,
+                float *keep_ds, float *keep_dr, unsigned *flags, cudaStream_t st) {
+    const int smem = Stage<T, DKT>::count(a.dv) * Stage<T, DKT>::bytes(a.dv) + 256;
+    cudaError_t e = cudaFuncSetAttribute(k_delta_backward<T, DKT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const unsigned char *units = (const unsigned char *)ws;
+    k_delta_backward<T, DKT><<<a.n * a.hv, kThreads, smem, st>>>(
+        a, (const T *)dout, dlast, dinit, units, units + (size_t)slots(a.tokens, a.n) * a.hv * kUnitBytes, (T *)dv,
+        keep_ds, keep_dr, flags);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_delta_backward(int dtype, const DeltaArgs &a, const void *dout, const float *dlast, float *dinit,
+                                  const void *ws, void *dv, float *keep_ds, float *keep_dr, unsigned *flags,
+                                  cudaStream_t st) {
+    const bool wide = a.dk > 64;
+    if (dtype == S4_BF16)
+        return wide ? run<__nv_bfloat16, 128>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st)
+                    : run<__nv_bfloat16, 64>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st);
+    if (dtype == S4_F16)
+        return wide ? run<__half, 128>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st)
+                    : run<__half, 64>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st);
+    return wide ? run<float, 128>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st)
+                : run<float, 64>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st);
+}
+
+}  // namespace s4

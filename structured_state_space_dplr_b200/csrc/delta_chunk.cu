@@ -25,8 +25,6 @@ namespace {
 
 using namespace delta;
 
-constexpr int kEpiWarps = 8, kLoadWarps = 3, kThreads = (kEpiWarps + 1 + kLoadWarps) * 32;
-
 // Tensor-memory columns. An operand's high and middle parts take the place of
 // the accumulator it was computed from, 16 columns by 16 columns, so a warp
 // overwrites only what it alone has read:
@@ -36,58 +34,7 @@ constexpr int kEpiWarps = 8, kLoadWarps = 3, kThreads = (kEpiWarps + 1 + kLoadWa
 //   kTmQ, kTmO   S0^T Q^T and (PT R)^T (64 each)
 constexpr int kTmS = 0, kTmSl = 128, kTmK = 192, kTmE = 256, kTmQ = 320, kTmO = 384, kTmRl = 448, kTmEl = 480;
 
-// parts of [K; Q], 128 rows; then T and PT and factors, V as it is
-template <typename T, int DKT>
-struct Stage {
-    static constexpr int NB = Parts<T>::n;
-    static constexpr int kImg = 2 * kC * DKT * 2, kTp = NB * kImg, kV = kTp + kUnitBytes;
-    static __host__ __device__ int bytes(int dv) { return kV + kC * dv * (int)sizeof(T); }
-    static __host__ __device__ int count(int dv) { return 2 * bytes(dv) + 256 <= 232448 ? 2 : 1; }
-};
-
 enum { bFull = 0, bEmpty = 2, bS = 4, bR = 8, bE = 10, bO = 12, bM1, bM2, bMq, bM2o, bM3, bCount };
-
-// 16 tokens of this lane's channel to o, `row` elements apart, the first n of
-// them. 16-bit types: neighbouring lanes swap so that each stores two channels
-// of every other token in one word (dv is even: both channels are there or not).
-template <typename T>
-__device__ __forceinline__ void store16(T *o, long long row, const float (&x)[16], int lane, bool vin, int n) {
-    if constexpr (sizeof(T) == 4) {
-        if (vin) {
-            if (n >= 16) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j * row] = x[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (j < n) o[j * row] = x[j];
-            }
-        }
-    } else {
-        const bool odd = lane & 1;
-        Pack<T, 2> w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? x[2 * j] : x[2 * j + 1], 1);
-            w[j].v[0] = from_f<T>(odd ? other : x[2 * j]);
-            w[j].v[1] = from_f<T>(odd ? x[2 * j + 1] : other);
-        }
-        if (odd) {   // the odd lane has the second token of each pair
-            o += row - 1;
-            --n;
-        }
-        if (vin) {
-            if (n >= 15) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) *reinterpret_cast<Pack<T, 2> *>(o + 2 * j * row) = w[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (2 * j < n) *reinterpret_cast<Pack<T, 2> *>(o + 2 * j * row) = w[j];
-            }
-        }
-    }
-}
 
 template <typename T, int DKT>
 __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, const float *init, float *last,
@@ -125,31 +72,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
         // ------------------------------------------------------ loading ----
         const int lt = tid - (kEpiWarps + 1) * 32;
         for (int c = 0, st = 0, turn = 0; c < chunks; ++c) {
-            unsigned char *sp = smem + st * stage_bytes;
-            const long long tok = sq.tok0 + (long long)c * kC;
-            const int rows = sq.len - c * kC < kC ? sq.len - c * kC : kC;
-            const T *vp = (const T *)a.v + tok * a.sv + (long long)hv * a.dv;
-            const unsigned char *up = ws + (size_t)((sq.slot0 + c) * a.hv + hv) * kUnitBytes;
-            const unsigned char *ip = images + (size_t)((sq.slot0 + c) * a.hk + hk) * L::kTp;
-            if (c + 1 < chunks) {   // the next chunk on its way to L2
-                if (lt < kC && lt < sq.len - (c + 1) * kC) {
-                    const char *p = (const char *)(vp + (kC + lt) * a.sv);
-                    for (int i = 0; i < a.dv * (int)sizeof(T); i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
-                }
-                if (lt == kC) {
-                    bulk_prefetch(up + (size_t)a.hv * kUnitBytes, kUnitBytes);
-                    bulk_prefetch(ip + (size_t)a.hk * L::kTp, L::kTp);
-                }
-            }
+            const long long slot = sq.slot0 + c;
+            const unsigned char *up = ws + (size_t)(slot * a.hv + hv) * kUnitBytes;
+            const unsigned char *ip = images + (size_t)(slot * a.hk + hk) * L::kTp;
+            const T *vp = (const T *)a.v + (sq.tok0 + (long long)c * kC) * a.sv + (long long)hv * a.dv;
+            if (c + 1 < chunks)
+                prefetch_stage<T, DKT>(ip + (size_t)a.hk * L::kTp, up + (size_t)a.hv * kUnitBytes, vp + kC * a.sv, a.sv,
+                                       sq.len - (c + 1) * kC, a.dv, lt);
             ok = umma::mbar_wait(bars + bEmpty + st, (turn & 1) ^ 1, kSpinLimit);   // the first use needs no wait
             if (!ok) break;
-            if (lt == 0) {
-                mbar_expect(bars + bFull + st, kUnitBytes + L::kTp);
-                bulk_load(sp, ip, L::kTp, bars + bFull + st);
-                bulk_load(sp + L::kTp, up, kUnitBytes, bars + bFull + st);
-                mbar_arrive(bars + bFull + st);
-            }
-            load_rows<T>(sp + L::kV, vp, a.sv, rows, a.dv, lt, kLoadWarps * 32, bars + bFull + st);
+            load_stage<T, DKT>(smem + st * stage_bytes, ip, up, vp, a.sv, sq.len - c * kC, a.dv, lt, bars + bFull + st);
             if (++st == ST) {
                 st = 0;
                 ++turn;
@@ -327,12 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
             // lanes past dv compute what channel 0 would be; nothing of it is stored
             const T *vs = reinterpret_cast<const T *>(sp + L::kV) + (vin ? v : 0);
             const long long unit = (sq.slot0 + c) * a.hv + hv;
-            if (keep_s && vin) {   // the state before the chunk
-                float *ks = keep_s + (size_t)unit * a.dk * a.dv + v;
-#pragma unroll
-                for (int i = 0; i < HC; ++i)
-                    if (h * HC + i < a.dk) ks[(size_t)(h * HC + i) * a.dv] = S[i];
-            }
+            if (keep_s && vin) store_state<HC>(keep_s + (size_t)unit * a.dk * a.dv, S, h, v, a.dk, a.dv);
             if (c > 0) put_output(c - 1, before);
             ok = ok && umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit) &&
                  umma::mbar_wait(bars + bM1, pc, kSpinLimit);
@@ -360,11 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 float x[16], e[16];
                 get16(eg + kC + j0, e);
                 tm_ld16(mine + kTmE + j0, x);
-                if (keep_e && vin) {
-                    float *ke = keep_e + ((size_t)unit * kC + j0) * a.dv + v;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) ke[(size_t)j * a.dv] = x[j];
-                }
+                if (keep_e && vin) store_tokens(keep_e + (size_t)unit * kC * a.dv, x, j0, v);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) x[j] *= e[j];
                 tm_split16(mine + kTmE + j0, mine + kTmEl + j0 / 2, x);

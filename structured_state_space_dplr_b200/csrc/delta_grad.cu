@@ -1,0 +1,498 @@
+// delta_grad.cu -- the chunked gated delta rule, backward within the chunks:
+// the gradients of q, k, beta and g from the states before the chunks (S0),
+// the state gradients behind them (dS1), E of the forward chain and dR of the
+// backward chain. Per chunk and value head, with F = dO E^T, X = dR E^T,
+// H_j = dS1 E_j and d_ij = e^(G_i - G_j):
+//     M_ij = scale beta_j d_ij F_ij (j <= i),  N_ij = beta_j d_ij X_ij (j < i)
+//     dq = scale e^G dO S0^T + M K
+//     dk = -e^G dR S0^T + beta e^(G_C - G) H - (N + N^T) K + M^T Q
+//     c1_j = sum_i scale d_ij q_i.k_j F_ij,  c2_j = sum_i d_ij k_i.k_j X_ij,
+//     h_j = e^(G_C - G_j) k_j.H_j,   dbeta = c1 + h - c2
+//     u_i = e^(G_i) (scale q_i.(S0 dO_i) - k_i.(S0 dR_i)),  W_ij the term of
+//     beta_j (c1_j - c2_j) with row i,
+//     dg_t = sum_{i >= t, j < t} W_ij + sum_{i >= t} u_i + sum_{j < t} beta_j h_j + e^(G_C) <S0, dS1>:
+// what passes from before t to t or behind (the terms of the decay's sums on
+// one side of t only cancel, and are left out).
+//
+// One block per chunk and key head, its value heads one after the other (their
+// dq and dk are summed in registers, in order). Tensor-memory lane = row of the
+// stacked [dR; dO], so dR's and dO's products share the instructions and the
+// scalings of rows are scalings of threads. Bound by memory: S0, dS1, E and dR
+// are 192 KB in float at Dk = Dv = 128, read once; they are split into bf16
+// parts here.
+#include "delta.cuh"
+#include "s4dplr.h"
+
+namespace s4 {
+namespace {
+
+using namespace delta;
+
+constexpr int kGradThreads = 256;
+constexpr int kTrLd = kC + 1;
+
+// tensor-memory columns: the left operands' parts, X and F, [dR; dO] S0^T (later the sum of the last products), E dS1^T
+constexpr int kTmA = 0, kTmXF = 192, kTmD = 256, kTmH = 384;
+
+template <typename T, int DKT, int DVT>
+struct GradSmem {
+    static constexpr int kS = DVT * DKT * 2, kE = kC * DVT * 2, kKq = kq_bytes<T, DKT>();   // one part of S0 or dS1, of E; all of [K; Q]
+    static constexpr int kSmall = 2 * kC * kTrLd * 4 + kC * 8 + 19 * kC * 4 + 128;
+    // [K; Q] stays beside the states' image where there is room for both
+    static constexpr bool kBeside = 3 * kS + 3 * kE + kKq + kSmall <= 232448;
+    static constexpr int kArea = kBeside ? 3 * kS + kKq : (3 * kS > kKq ? 3 * kS : kKq);
+    static constexpr int kOffKq = kBeside ? 3 * kS : 0, kOffE = kArea, kOffSmall = kArea + 3 * kE;
+    static constexpr int kBytes = kOffSmall + kSmall;
+    static_assert(kBytes <= 232448, "shared memory of a block");
+};
+
+// 8 floats at p as three parts of 16 bytes, `part` bytes apart at dst
+__device__ __forceinline__ void put_parts(unsigned char *dst, int part, const float (&f)[8]) {
+    uint32_t w[4][3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split<3>(f[2 * i], f[2 * i + 1], w[i]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+        *reinterpret_cast<uint4 *>(dst + q * part) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+}
+__device__ __forceinline__ void get8(const float *p, float (&f)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+// sums over the warp: lane l ends with the sum of the lanes' w[l] in w[0]
+__device__ __forceinline__ void column_sums(float (&w)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int t = 0; t < o; ++t) {
+            const bool up = lane & o;
+            const float other = __shfl_xor_sync(0xffffffffu, up ? w[t] : w[t + o], o);
+            w[t] = (up ? w[t + o] : w[t]) + other;
+        }
+}
+
+template <typename T>
+__device__ __forceinline__ void get8(const T *p, float (&f)[8]) {   // 16-bit types
+    load_pack<T, 8>(p, f);
+}
+
+template <typename T, int DKT, int DVT>
+__global__ void __launch_bounds__(kGradThreads, 1)
+    k_delta_gradient(DeltaArgs a, const T *dout, const unsigned char *images, const float *keep_s, const float *keep_e,
+                     const float *keep_ds, const float *keep_dr, T *dq, T *dk, float *dg, float *dbeta,
+                     unsigned *flags) {
+    using L = GradSmem<T, DKT, DVT>;
+    constexpr int NB = Parts<T>::n, kPart = 2 * kC * DKT * 2, HK = DKT / 2, KV = DVT / 16;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char *kq = smem + L::kOffKq, *ei = smem + L::kOffE;
+    float *tr = reinterpret_cast<float *>(smem + L::kOffSmall);              // N, M: [2][64][65]
+    float2 *Gs = reinterpret_cast<float2 *>(tr + 2 * kC * kTrLd);
+    float *bs = reinterpret_cast<float *>(Gs + kC);                          // beta
+    float *eg = bs + kC, *dec = eg + kC;                                     // e^G, e^(G_C - G)
+    float *csum = dec + kC;                                                  // [4][64]
+    float *gsum = csum + 4 * kC, *rsum = gsum + 4 * kC;                      // [4][64], [128]
+    float *dot = rsum + 2 * kC, *hdot = dot + 4 * kC;                        // [2][128], [2][64]
+    float *red = hdot + 2 * kC;                                              // [8]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(red + 8);                  // kq, two products in flight
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 3);
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    const int R = (warp & 3) * 32 + lane, i = R & (kC - 1), half = warp >> 2;   // row of [dR; dO] and of [K; Q], its token
+    const bool low = R < kC;                                                    // a row of dR and K
+
+    const long long slot = blockIdx.x / a.hk;
+    const int hk = blockIdx.x % a.hk, per = a.hv / a.hk;
+    const Chunk ch = chunk_of(a, slot);
+    if (ch.rows <= 0) return;   // a slot no chunk uses
+    const int rows = ch.rows;
+    const long long tok = ch.tok;
+    const long long orow = (long long)a.hv * a.dv;
+
+    if (warp == 0) umma::tmem_alloc(tslot, 512);
+    if (tid == 0) {
+        for (int n = 0; n < 3; ++n) umma::mbar_init(bars + n, 1);
+        umma::fence_mbar_init();
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tm = uniform(*tslot);
+    const uint32_t mine = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s0 = saddr(smem), kq0 = saddr(kq), e0 = saddr(ei);
+    int kq_turn = 0, turn1 = 0, turn2 = 0;
+    bool ok = true;
+    auto load_kq = [&]() {   // behind a barrier of the block; every thread waits
+        if (tid == 0) {
+            mbar_expect(bars, L::kKq);
+            bulk_load(kq, images + (size_t)(slot * a.hk + hk) * L::kKq, L::kKq, bars);
+            mbar_arrive(bars);
+        }
+        ok = umma::mbar_wait(bars, kq_turn++ & 1, kSpinLimit) && ok;
+    };
+    auto barrier = [&]() {   // operands written by these threads before, products (and bulk loads) behind
+        tm_wait_st();
+        umma::fence_proxy_async();
+        umma::fence_before_sync();
+        __syncthreads();
+        umma::fence_after_sync();
+    };
+    auto wait1 = [&]() {
+        ok = umma::mbar_wait(bars + 1, turn1++ & 1, kSpinLimit) && ok;
+        umma::fence_after_sync();
+    };
+    auto wait2 = [&]() {
+        ok = umma::mbar_wait(bars + 2, turn2++ & 1, kSpinLimit) && ok;
+        umma::fence_after_sync();
+    };
+    // (+)= A [parts of K = 16 KS columns at kTmA] times an image's parts; n columns
+    auto times = [&](uint32_t d, uint32_t at, uint32_t lo, int ks_n, uint64_t b, uint32_t part, uint32_t step, uint32_t id,
+                     int nb, bool first) {
+#pragma unroll
+        for (int o = 2; o >= 0; --o)
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                if (o - j < 0 || j >= nb) continue;
+                const int p = o - j;
+                for (int ks = 0; ks < ks_n; ++ks) {
+                    mma_ts(tm + d, tm + (p < 2 ? at + 16 * ks + 8 * p : lo + 8 * ks),
+                           b + ((uint64_t)(j * part + ks * step) >> 4), id, !first);
+                    first = false;
+                }
+            }
+    };
+
+    // q_i.k_j and k_i.k_j, the same for all value heads
+    load_kq();
+    float raw[kC / 2];
+    if (warp == 0) {
+        if (elect()) {
+            bool acc = false;
+#pragma unroll
+            for (int o = 2; o >= 0; --o)
+#pragma unroll
+                for (int p = 0; p < NB; ++p) {
+                    const int j = o - p;
+                    if (j < 0 || j >= NB) continue;
+#pragma unroll
+                    for (int ks = 0; ks < DKT / 16; ++ks) {
+                        umma::mma_bf16(tm + kTmXF, desc_k(kq0 + p * kPart + ks * 4096, 2048, 128),
+                                       desc_k(kq0 + j * kPart + ks * 4096, 2048, 128), idesc(kC, false, false), acc);
+                        acc = true;
+                    }
+                }
+            umma::commit(bars + 1);
+        }
+        __syncwarp();
+    }
+    wait1();
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        float x[16];
+        tm_ld16(mine + kTmXF + half * (kC / 2) + 16 * n, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) raw[16 * n + j] = x[j];
+    }
+    float acc[HK];   // this row of dk or dq, half of the columns
+#pragma unroll
+    for (int n = 0; n < HK; ++n) acc[n] = 0.0f;
+
+    for (int g = 0; g < per; ++g) {
+        const int hv = hk * per + g;
+        const long long unit = slot * a.hv + hv;
+        const float *us = keep_s + (size_t)unit * a.dk * a.dv, *ud = keep_ds + (size_t)unit * a.dk * a.dv;
+        const float *ue = keep_e + (size_t)unit * kC * a.dv, *ur = keep_dr + (size_t)unit * kC * a.dv;
+        barrier();   // the last head's reads of shared and tensor memory
+        if (tid == 0) bulk_prefetch(ud, (uint32_t)(a.dk * a.dv) * 4);
+        if (warp == 1) {
+            const GateSums gt = gate_sums(a, tok, hv, rows, lane);
+            const int j = 2 * lane;
+            const float xf = (float)gt.x, yf = (float)gt.y;
+            Gs[j] = make_float2(xf, (float)(gt.x - xf));
+            Gs[j + 1] = make_float2(yf, (float)(gt.y - yf));
+            bs[j] = gt.b0;
+            bs[j + 1] = gt.b1;
+            const double all = __shfl_sync(0xffffffffu, gt.y, 31);
+            eg[j] = exp2f(xf);
+            eg[j + 1] = exp2f(yf);
+            dec[j] = exp2f((float)(all - gt.x));
+            dec[j + 1] = exp2f((float)(all - gt.y));
+        }
+        // E as right operand: rows tokens, K = v
+        for (int n = tid; n < kC * DVT / 8; n += kGradThreads) {
+            const int t = n & (kC - 1), vg = n / kC;
+            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (8 * vg < a.dv) get8(ue + (size_t)n * 8, f);
+            put_parts(ei + (t >> 3) * 128 + vg * 1024 + (t & 7) * 16, L::kE, f);
+        }
+        // S0 as right operand: columns dk, K = v
+        for (int n = tid; n < DVT * DKT / 8; n += kGradThreads) {
+            const int v = n & (DVT - 1), dgr = n / DVT;
+            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (v < a.dv && 8 * dgr < a.dk) get8(us + ((size_t)dgr * a.dv + v) * 8, f);
+            put_parts(smem + (v >> 3) * 128 + dgr * (DVT * 16) + (v & 7) * 16, L::kS, f);
+        }
+        // [dR; dO] as left operand, half of the columns a thread
+#pragma unroll
+        for (int n = 0; n < KV / 2; ++n) {
+            const int ks = half * (KV / 2) + n;
+            float x[16];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int v = 16 * ks + 8 * m;
+                float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (v < a.dv) {
+                    if (low)
+                        get8(ur + ((size_t)(v >> 3) * kC + i) * 8, f);
+                    else if (i < rows)
+                        get8(dout + (tok + i) * orow + (long long)hv * a.dv + v, f);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[8 * m + j] = f[j];
+            }
+            tm_split16(mine + kTmA + 16 * ks, mine + kTmA + DVT + 8 * ks, x);
+        }
+        barrier();
+        if (warp == 0) {
+            if (elect()) {
+                times(kTmXF, kTmA, kTmA + DVT, KV, desc_k(e0, 1024, 128), L::kE, 2048, idesc(kC, false, false), 3, true);
+                umma::commit(bars + 1);
+                times(kTmD, kTmA, kTmA + DVT, KV, desc_mn(s0, 128, DVT * 16), L::kS, 256, idesc(DKT, false, true), 3, true);
+                umma::commit(bars + 2);
+            }
+            __syncwarp();
+        }
+        wait1();
+        float m[kC / 2];   // row i of N or M
+        {
+            const float2 Gi = Gs[i];
+            const float mul = low ? 1.0f : a.scale;
+            float cw[kC / 2], pw[kC / 2], rs = 0.0f;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int j0 = half * (kC / 2) + 16 * n;
+                float x[16];
+                tm_ld16(mine + kTmXF + j0, x);
+#pragma unroll
+                for (int t = 0; t < 16; ++t) {
+                    const int j = j0 + t;
+                    const float2 Gj = Gs[j];
+                    const bool in = low ? j < i : j <= i;
+                    const float w = in ? x[t] * mul * exp2f((Gi.x - Gj.x) + (Gi.y - Gj.y)) : 0.0f;
+                    cw[16 * n + t] = w * raw[16 * n + t];
+                    pw[16 * n + t] = j <= i ? rs : 0.0f;   // what this half's columns before j hand to row i >= j
+                    rs = fmaf(bs[j], cw[16 * n + t], rs);
+                    m[16 * n + t] = bs[j] * w;
+                    tr[((low ? 0 : kC) + i) * kTrLd + j] = m[16 * n + t];
+                }
+            }
+            if (half == 0) rsum[R] = rs;
+            column_sums(cw, lane);
+            column_sums(pw, lane);
+            csum[(warp & 3) * kC + half * (kC / 2) + lane] = cw[0];
+            gsum[(warp & 3) * kC + half * (kC / 2) + lane] = pw[0];
+        }
+        wait2();   // the left operand and S0 are used up
+        if (low) {   // E as left operand (rows 64-127 of the product go unread)
+#pragma unroll
+            for (int n = 0; n < KV / 2; ++n) {
+                const int ks = half * (KV / 2) + n;
+                const unsigned char *src = ei + (i >> 3) * 128 + 2 * ks * 1024 + (i & 7) * 16;
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(src + p * L::kE);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + p * L::kE + 1024);
+                    const uint32_t r[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+                    tm_st8(mine + kTmA + (p < 2 ? 16 * ks + 8 * p : DVT + 8 * ks), r);
+                }
+            }
+        }
+        float both = 0.0f;   // <S0, dS1>
+        for (int n = tid; n < DVT * DKT / 8; n += kGradThreads) {
+            const int v = n & (DVT - 1), dgr = n / DVT;
+            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (v < a.dv && 8 * dgr < a.dk) {
+                float z[8];
+                get8(ud + ((size_t)dgr * a.dv + v) * 8, f);
+                get8(us + ((size_t)dgr * a.dv + v) * 8, z);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) both = fmaf(f[j], z[j], both);
+            }
+            put_parts(smem + (v >> 3) * 128 + dgr * (DVT * 16) + (v & 7) * 16, L::kS, f);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) both += __shfl_xor_sync(0xffffffffu, both, o);
+        if (lane == 0) red[warp] = both;
+        barrier();
+        if (warp == 0) {
+            if (elect()) {
+                times(kTmH, kTmA, kTmA + DVT, KV, desc_mn(s0, 128, DVT * 16), L::kS, 256, idesc(DKT, false, true), 3, true);
+                umma::commit(bars + 1);
+            }
+            __syncwarp();
+        }
+        wait1();
+        if constexpr (!L::kBeside) {
+            barrier();
+            load_kq();
+        }
+        // left operands of the products with K (-(N + N^T); M) and Q (M^T; 0)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int j0 = half * (kC / 2) + 16 * n;
+            float x[16], y[16];
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+                const int j = j0 + t;
+                x[t] = low ? -(m[16 * n + t] + tr[j * kTrLd + i]) : m[16 * n + t];
+                y[t] = low ? tr[(kC + j) * kTrLd + i] : 0.0f;
+            }
+            tm_split16(mine + kTmA + j0, mine + kTmA + 64 + j0 / 2, x);
+            tm_split16(mine + kTmA + 96 + j0, mine + kTmA + 160 + j0 / 2, y);
+        }
+        // the products with the states: into dk or dq, and their dots with k or q
+        {
+            const float sr = low ? -eg[i] : a.scale * eg[i], hr = bs[i] * dec[i];
+            float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+            for (int n = 0; n < HK; n += 16) {
+                const int d = half * HK + n;
+                float x[16], y[16], k[16];
+                tm_ld16(mine + kTmD + d, x);
+                tm_ld16(mine + kTmH + d, y);
+                const unsigned char *src = kq + (R >> 3) * 128 + (d >> 3) * 2048 + (R & 7) * 16;
+#pragma unroll
+                for (int t = 0; t < 16; ++t) k[t] = 0.0f;
+#pragma unroll
+                for (int p = NB - 1; p >= 0; --p)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(src + p * kPart + q * 2048);
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            k[8 * q + 2 * t] += lo_f(w[t]);
+                            k[8 * q + 2 * t + 1] += hi_f(w[t]);
+                        }
+                    }
+#pragma unroll
+                for (int t = 0; t < 16; ++t) {
+                    d0 = fmaf(x[t], k[t], d0);
+                    acc[n + t] = fmaf(sr, x[t], acc[n + t]);
+                    if (low) {
+                        d1 = fmaf(y[t], k[t], d1);
+                        acc[n + t] = fmaf(hr, y[t], acc[n + t]);
+                    }
+                }
+            }
+            dot[half * 2 * kC + R] = sr * d0;          // -e^G k.(S0 dR); scale e^G q.(S0 dO)
+            if (low) hdot[half * kC + i] = dec[i] * d1;
+        }
+        barrier();
+        if (warp == 0) {
+            if (elect()) {
+                times(kTmD, kTmA, kTmA + 64, kC / 16, desc_mn(kq0, 128, 2048), kPart, 256, idesc(DKT, false, true), NB, true);
+                times(kTmD, kTmA + 96, kTmA + 160, kC / 16, desc_mn(kq0 + 1024, 128, 2048), kPart, 256,
+                      idesc(DKT, false, true), NB, false);
+                umma::commit(bars + 2);
+            }
+            __syncwarp();
+        }
+        if (warp == 1) {   // dbeta and dg, two tokens a lane
+            float rect[2], u[2], r0[2], bh[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int j = 2 * lane + t;
+                const float c2 = csum[j] + csum[kC + j], c1 = csum[2 * kC + j] + csum[3 * kC + j];
+                const float hj = hdot[j] + hdot[kC + j];
+                if (j < rows) dbeta[(tok + j) * a.hv + hv] = (c1 - c2) + hj;
+                bh[t] = bs[j] * hj;
+                rect[t] = (gsum[2 * kC + j] + gsum[3 * kC + j]) - (gsum[j] + gsum[kC + j]);
+                u[t] = (dot[j] + dot[2 * kC + j]) + (dot[kC + j] + dot[3 * kC + j]);
+                r0[t] = rsum[kC + j] - rsum[j];   // of the first 32 columns: for t >= 32 they are all before t
+            }
+            float ss = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) ss += red[w];
+            // from this lane's first token on; before it
+            float su = u[0] + u[1], sr = r0[0] + r0[1], sb = bh[0] + bh[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float z0 = __shfl_down_sync(0xffffffffu, su, o), z1 = __shfl_down_sync(0xffffffffu, sr, o);
+                const float z2 = __shfl_up_sync(0xffffffffu, sb, o);
+                if (lane + o < 32) su += z0, sr += z1;
+                if (lane >= o) sb += z2;
+            }
+            sb = __shfl_up_sync(0xffffffffu, sb, 1);
+            if (lane == 0) sb = 0.0f;
+            const float all = eg[kC - 1] * ss;
+            const int j = 2 * lane;
+            const bool late = lane >= 16;
+            if (j < rows) dg[(tok + j) * a.hv + hv] = (rect[0] + (late ? sr : 0.0f)) + su + sb + all;
+            if (j + 1 < rows)
+                dg[(tok + j + 1) * a.hv + hv] =
+                    (rect[1] + (late ? sr - r0[0] : 0.0f)) + (su - u[0]) + (sb + bh[0]) + all;
+        }
+        wait2();
+#pragma unroll
+        for (int n = 0; n < HK; n += 16) {
+            float x[16];
+            tm_ld16(mine + kTmD + half * HK + n, x);
+#pragma unroll
+            for (int t = 0; t < 16; ++t) acc[n + t] += x[t];
+        }
+    }
+    if (i < rows) {
+        T *o = (low ? dk : dq) + ((tok + i) * a.hk + hk) * a.dk + half * HK;
+#pragma unroll
+        for (int n = 0; n < HK; n += 8)
+            if (half * HK + n < a.dk) {
+                const float f[8] = {acc[n],     acc[n + 1], acc[n + 2], acc[n + 3],
+                                    acc[n + 4], acc[n + 5], acc[n + 6], acc[n + 7]};
+                if constexpr (sizeof(T) == 2) {
+                    store_pack<T, 8>(o + n, f);
+                } else {
+                    *reinterpret_cast<float4 *>(o + n) = make_float4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<float4 *>(o + n + 4) = make_float4(f[4], f[5], f[6], f[7]);
+                }
+            }
+    }
+    if (!ok && flags && lane == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    if (warp == 0) umma::tmem_dealloc(tm, 512);
+}
+
+template <typename T, int DKT, int DVT>
+cudaError_t run(const DeltaArgs &a, const void *dout, const void *ws, const float *keep_s, const float *keep_e,
+                const float *keep_ds, const float *keep_dr, void *dq, void *dk, float *dg, float *dbeta,
+                unsigned *flags, cudaStream_t st) {
+    constexpr int smem = GradSmem<T, DKT, DVT>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(k_delta_gradient<T, DKT, DVT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const long long n = slots(a.tokens, a.n);
+    k_delta_gradient<T, DKT, DVT><<<(unsigned)(n * a.hk), kGradThreads, smem, st>>>(
+        a, (const T *)dout, (const unsigned char *)ws + (size_t)n * a.hv * kUnitBytes, keep_s, keep_e, keep_ds, keep_dr,
+        (T *)dq, (T *)dk, dg, dbeta, flags);
+    return cudaGetLastError();
+}
+
+template <typename T, typename... Args>
+cudaError_t by_size(const DeltaArgs &a, Args... args) {
+    if (a.dk > 64) return a.dv > 64 ? run<T, 128, 128>(a, args...) : run<T, 128, 64>(a, args...);
+    return a.dv > 64 ? run<T, 64, 128>(a, args...) : run<T, 64, 64>(a, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_delta_gradient(int dtype, const DeltaArgs &a, const void *dout, const void *ws, const float *keep_s,
+                                  const float *keep_e, const float *keep_ds, const float *keep_dr, void *dq, void *dk,
+                                  float *dg, float *dbeta, unsigned *flags, cudaStream_t st) {
+    if (dtype == S4_BF16)
+        return by_size<__nv_bfloat16>(a, dout, ws, keep_s, keep_e, keep_ds, keep_dr, dq, dk, dg, dbeta, flags, st);
+    if (dtype == S4_F16)
+        return by_size<__half>(a, dout, ws, keep_s, keep_e, keep_ds, keep_dr, dq, dk, dg, dbeta, flags, st);
+    return by_size<float>(a, dout, ws, keep_s, keep_e, keep_ds, keep_dr, dq, dk, dg, dbeta, flags, st);
+}
+
+}  // namespace s4

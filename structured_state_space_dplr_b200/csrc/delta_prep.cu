@@ -80,21 +80,10 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
 
     const long long slot = blockIdx.x / a.hv;
     const int hv = blockIdx.x % a.hv, per = a.hv / a.hk, hk = hv / per;
-    int s = 0;   // the last sequence that starts at or before the slot
-    for (int lo = 0, hi = a.n; lo < hi;) {
-        const int m = (lo + hi) >> 1;
-        if (sequence(a, m).slot0 <= slot) {
-            s = m;
-            lo = m + 1;
-        } else {
-            hi = m;
-        }
-    }
-    const Seq sq = sequence(a, s);
-    const long long c0 = (slot - sq.slot0) * kC;
-    if (c0 < 0 || c0 >= sq.len) return;   // a slot no chunk uses
-    const int rows = sq.len - c0 < kC ? (int)(sq.len - c0) : kC;
-    const long long tok = sq.tok0 + c0;
+    const Chunk ch = chunk_of(a, slot);
+    if (ch.rows <= 0) return;   // a slot no chunk uses
+    const int rows = ch.rows;
+    const long long tok = ch.tok;
 
     load_image<T, DKT>(smem, kPart, 2048, (const T *)a.k + tok * a.sk + (long long)hk * a.dk, a.sk, rows, a.dk, warp, 8);
     load_image<T, DKT>(smem + 1024, kPart, 2048, (const T *)a.q + tok * a.sq + (long long)hk * a.dk, a.sq, rows, a.dk,
@@ -104,25 +93,11 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
         umma::mbar_init(bar, 1);
         umma::fence_mbar_init();
     }
-    if (warp == 1) {   // running sums of g, in units of ln 2, in double
+    if (warp == 1) {
+        const GateSums gt = gate_sums(a, tok, hv, rows, lane);
         const int j = 2 * lane;
-        const long long at = tok * a.hv + hv;
-        float g0 = j < rows ? __ldg(a.g + at + (long long)j * a.hv) : 0.0f;
-        float g1 = j + 1 < rows ? __ldg(a.g + at + (long long)(j + 1) * a.hv) : 0.0f;
-        const float b0 = j < rows ? __ldg(a.beta + at + (long long)j * a.hv) : 0.0f;
-        const float b1 = j + 1 < rows ? __ldg(a.beta + at + (long long)(j + 1) * a.hv) : 0.0f;
-        // exp(-1e5) is 0 as exp(-inf) is, and differences stay numbers
-        g0 = g0 < -1e5f ? -1e5f : g0;
-        g1 = g1 < -1e5f ? -1e5f : g1;
-        constexpr double kLog2e = 1.4426950408889634;   // 1 / ln 2
-        const double d1 = (double)g1 * kLog2e;
-        double y = (double)g0 * kLog2e + d1;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
-        }
-        const double x = y - d1;
+        const double x = gt.x, y = gt.y;
+        const float b0 = gt.b0, b1 = gt.b1;
         const float xf = (float)x, yf = (float)y;
         Gs[j] = make_float2(xf, (float)(x - xf));
         Gs[j + 1] = make_float2(yf, (float)(y - yf));

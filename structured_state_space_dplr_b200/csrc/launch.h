@@ -117,6 +117,15 @@ cudaError_t launch_delta_prep(int dtype, const DeltaArgs &a, void *ws, unsigned 
 cudaError_t launch_delta_forward(int dtype, const DeltaArgs &a, const float *init, float *last, const void *ws,
                                  float *keep_s, float *keep_e, unsigned *flags, cudaStream_t st);
 
+// backward in the states: dV, the first states' gradient, keep_ds and keep_dr (behind every chunk, of every chunk)
+cudaError_t launch_delta_backward(int dtype, const DeltaArgs &a, const void *dout, const float *dlast, float *dinit,
+                                  const void *ws, void *dv, float *keep_ds, float *keep_dr, unsigned *flags,
+                                  cudaStream_t st);
+// the other gradients, from all that was kept
+cudaError_t launch_delta_gradient(int dtype, const DeltaArgs &a, const void *dout, const void *ws, const float *keep_s,
+                                  const float *keep_e, const float *keep_ds, const float *keep_dr, void *dq, void *dk,
+                                  float *dg, float *dbeta, unsigned *flags, cudaStream_t st);
+
 // ---- decode.cu ----
 cudaError_t launch_dplr_discretize(const float2 *Lambda, const float2 *P, const float2 *Q,
                                    const float2 *B, const float2 *C, const float *log_dt, int H, int Nh,

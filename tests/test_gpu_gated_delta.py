@@ -22,7 +22,7 @@ NAMES = ("q", "k", "v", "g", "beta")
 REL = 4.5e-6
 
 
-def check(got, ref, dtype, what, terms=None):
+def check(got, ref, dtype, what, passes=1):
     torch = torch_cuda()
     step = torch.finfo(dtype).eps / 2 if dtype != torch.float32 else 0.0
     real = ~np.isnan(ref)
@@ -33,10 +33,12 @@ def check(got, ref, dtype, what, terms=None):
     norm = np.linalg.norm(r)
     err = np.linalg.norm(g - r)
     # the norm of the roundings to 16 bits is at most a half step of each value
-    assert err <= (REL + step) * norm + 1e-30, f"{what}: {err / norm}"
+    assert err <= (passes * REL + step) * norm + 1e-30, f"{what}: {err} of {norm}"
+    if norm == 0.0:      # then the values are zeros, as the line above says
+        return
     rms = norm / np.sqrt(r.size)
     big = (np.abs(g - r) / np.maximum(np.abs(r), rms)).max()
-    assert big <= 1.01 * step + 16 * REL, f"{what}: one value {big}"
+    assert big <= 1.01 * step + 16 * passes * REL, f"{what}: one value {big}"
 
 
 def forward(d, **more):
@@ -69,3 +71,40 @@ def test_forward(shape, dtype):
         o, got, _ = forward(d, scale=0.7, initial_state=d["state"], keep=keep)
         check(o, ref, d["v"].dtype, "o from a state")
         check(got, last, torch.float32, "state from a state")
+
+
+def backward(d, do, work, **more):
+    import structured_state_space_dplr_b200 as s4
+    torch = torch_cuda()
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = s4.gated_delta_backward(*(d[n] for n in NAMES), do, work, flags=flags, **more)
+    assert flags.item() == 0
+    return r
+
+
+def gen(seed):
+    torch = torch_cuda()
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+def test_backward(shape, dtype):
+    torch = torch_cuda()
+    d = make(*shape, dtype=dtype)
+    do = torch.randn(d["v"].shape, device="cuda", generator=gen(1)).to(d["v"].dtype)
+    ds = torch.randn(d["state"].shape, device="cuda", generator=gen(2))
+    args = [f64(d[n]) for n in NAMES]
+    _, _, ref = delta.gated_delta(*args, 0.7, f64(d["state"]), do=f64(do), dstate=f64(ds))
+    _, _, work = forward(d, scale=0.7, initial_state=d["state"], keep=True)
+    got = backward(d, do, work, scale=0.7, dfinal_state=ds)
+    # a gradient passes the forward chain, the backward chain and three more products: twice the forward's error
+    for m in (*NAMES, "initial_state"):
+        check(got[m], ref[m], got[m].dtype, "d" + m, 2)
+    again = backward(d, do, work, scale=0.7, dfinal_state=ds)
+    assert all(torch.equal(got[m], again[m]) for m in got)     # the workspace is not used up, the bits are the same
+    _, _, ref = delta.gated_delta(*args, shape[4] ** -0.5, do=f64(do))
+    _, _, work = forward(d, keep=True)
+    got = backward(d, do, work)
+    for m in NAMES:
+        check(got[m], ref[m], got[m].dtype, "d" + m + " from zero", 2)

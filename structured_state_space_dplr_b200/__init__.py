@@ -595,23 +595,68 @@ def recurrent_scan(Abar, Bbar, C, D, x, u, *, out=None, mode=None):
 
 
 # ------------------------------------------- token-major operators ----
+# These calls can be a few microseconds on the GPU, so their checks take the
+# short way to the same facts as _cuda's.
 _DTYPES = {torch.float32: _lib.S4_F32, torch.bfloat16: _lib.S4_BF16, torch.float16: _lib.S4_F16}
+_F32 = torch.float32
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _dtype(t, name):
-    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be a float32, bfloat16 or float16 tensor")
-    return _DTYPES[t.dtype]
+def _kind(t, name):
+    """The s4_dtype of a CUDA tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    kind = _DTYPES.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return kind
 
 
-def _buffer(t, name, shape, dtype, device):
+def _on(t, name, dtype, dev):
+    """Raises unless t is a CUDA tensor of the type on the current device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current CUDA device is cuda:{dev} "
+                         f"(use torch.cuda.device({t.device}))")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _full(t, name, shape, dtype, dev):
+    """t's address, after checking type, device, shape and layout."""
+    _on(t, name, dtype, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _out(t, name, shape, dtype, dev):
     """t, checked, or a new tensor where it is None."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _cuda(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    _full(t, name, shape, dtype, dev)
     return t
+
+
+def _scratch(t, need, dev):
+    """The caller's workspace, or a new one of `need` bytes."""
+    if t is None:
+        return torch.empty(need, dtype=torch.uint8, device="cuda")
+    _on(t, "workspace", torch.uint8, dev)
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t
+
+
+def _flag_word(flags, dev):
+    if flags is None:
+        return None
+    _on(flags, "flags", torch.int32, dev)
+    return flags.data_ptr()
 
 
 def layernorm(x, gamma, beta, eps=1e-5, *, out=None, mean=None, rstd=None):
@@ -619,108 +664,116 @@ def layernorm(x, gamma, beta, eps=1e-5, *, out=None, mean=None, rstd=None):
     float16; gamma, beta [D] float32; s4_layernorm). Returns (z, mean, rstd):
     z of x's type, mean and rstd [...] float32 for layernorm_backward. out may
     be x."""
-    kind = _dtype(x, "x")
-    _cuda(x, "x")
-    D = x.shape[-1]
-    _buffer(_cuda(gamma, "gamma"), "gamma", (D,), torch.float32, x.device)
-    _buffer(_cuda(beta, "beta"), "beta", (D,), torch.float32, x.device)
-    out = _buffer(out, "out", x.shape, x.dtype, x.device)
-    mean = _buffer(mean, "mean", x.shape[:-1], torch.float32, x.device)
-    rstd = _buffer(rstd, "rstd", x.shape[:-1], torch.float32, x.device)
-    _lib.call("s4_layernorm", kind, _ptr(x), _ptr(gamma), _ptr(beta), float(eps), mean.numel(), D, _ptr(out),
-              _ptr(mean), _ptr(rstd), _stream())
+    kind, dev = _kind(x, "x"), _current_device()
+    shape, dtype = x.shape, x.dtype
+    lead, D = shape[:-1], shape[-1]
+    xp = _full(x, "x", shape, dtype, dev)
+    gp, bp = _full(gamma, "gamma", (D,), _F32, dev), _full(beta, "beta", (D,), _F32, dev)
+    out = _out(out, "out", shape, dtype, dev)
+    mean, rstd = _out(mean, "mean", lead, _F32, dev), _out(rstd, "rstd", lead, _F32, dev)
+    _lib.call("s4_layernorm", kind, xp, gp, bp, eps, mean.numel(), D, out.data_ptr(), mean.data_ptr(),
+              rstd.data_ptr(), _current_stream(dev))
     return out, mean, rstd
+
+
+_norm_bytes = {}
 
 
 def layernorm_backward_workspace_size(D) -> int:
     """Bytes of workspace layernorm_backward (or, with D = H,
     layernorm_channels_backward) needs."""
-    n = ctypes.c_size_t(0)
-    _lib.call("s4_layernorm_backward_workspace_size", int(D), ctypes.byref(n))
-    return n.value
-
-
-def _norm_workspace(D, device, workspace):
-    if workspace is None:
-        workspace = torch.empty(layernorm_backward_workspace_size(D), dtype=torch.uint8, device=device)
-    return _cuda(workspace, "workspace", torch.uint8)
+    if D not in _norm_bytes:
+        n = ctypes.c_size_t(0)
+        _lib.call("s4_layernorm_backward_workspace_size", int(D), ctypes.byref(n))
+        _norm_bytes[D] = n.value
+    return _norm_bytes[D]
 
 
 def layernorm_backward(dz, x, gamma, mean, rstd, *, dx=None, dgamma=None, dbeta=None, workspace=None):
     """Backward of layernorm (s4_layernorm_backward): returns (dx of x's type,
     dgamma, dbeta [D] float32). dx may be dz."""
-    kind = _dtype(x, "x")
-    _cuda(x, "x")
-    D = x.shape[-1]
-    _buffer(_cuda(dz, "dz"), "dz", x.shape, x.dtype, x.device)
-    _buffer(_cuda(gamma, "gamma"), "gamma", (D,), torch.float32, x.device)
-    _buffer(_cuda(mean, "mean"), "mean", x.shape[:-1], torch.float32, x.device)
-    _buffer(_cuda(rstd, "rstd"), "rstd", x.shape[:-1], torch.float32, x.device)
-    dx = _buffer(dx, "dx", x.shape, x.dtype, x.device)
-    dgamma = _buffer(dgamma, "dgamma", (D,), torch.float32, x.device)
-    dbeta = _buffer(dbeta, "dbeta", (D,), torch.float32, x.device)
-    workspace = _norm_workspace(D, x.device, workspace)
-    _lib.call("s4_layernorm_backward", kind, _ptr(dz), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), mean.numel(), D,
-              _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace.numel(), _stream())
+    kind, dev = _kind(x, "x"), _current_device()
+    shape, dtype = x.shape, x.dtype
+    lead, D = shape[:-1], shape[-1]
+    xp, zp = _full(x, "x", shape, dtype, dev), _full(dz, "dz", shape, dtype, dev)
+    gp, mp, rp = (_full(gamma, "gamma", (D,), _F32, dev), _full(mean, "mean", lead, _F32, dev),
+                  _full(rstd, "rstd", lead, _F32, dev))
+    dx = _out(dx, "dx", shape, dtype, dev)
+    dgamma, dbeta = _out(dgamma, "dgamma", (D,), _F32, dev), _out(dbeta, "dbeta", (D,), _F32, dev)
+    workspace = _scratch(workspace, layernorm_backward_workspace_size(D), dev)
+    _lib.call("s4_layernorm_backward", kind, zp, xp, gp, mp, rp, mean.numel(), D, dx.data_ptr(), dgamma.data_ptr(),
+              dbeta.data_ptr(), workspace.data_ptr(), workspace.numel(), _current_stream(dev))
     return dx, dgamma, dbeta
 
 
 def layernorm_channels_backward(dz, x, gamma, eps=1e-5, *, dx=None, dgamma=None, dbeta=None, workspace=None):
     """Backward of layernorm_channels (s4_layernorm_channels_backward): dz, x
     [Bt, H, L] float32; returns (dx, dgamma [H], dbeta [H])."""
-    x = _cuda(x, "x", torch.float32)
+    dev = _current_device()
+    _on(x, "x", _F32, dev)
     if x.dim() != 3:
         raise ValueError("x must be [Bt, H, L]")
-    Bt, H, L = x.shape
-    _buffer(_cuda(dz, "dz"), "dz", x.shape, torch.float32, x.device)
-    _buffer(_cuda(gamma, "gamma"), "gamma", (H,), torch.float32, x.device)
-    dx = _buffer(dx, "dx", x.shape, torch.float32, x.device)
-    dgamma = _buffer(dgamma, "dgamma", (H,), torch.float32, x.device)
-    dbeta = _buffer(dbeta, "dbeta", (H,), torch.float32, x.device)
-    workspace = _norm_workspace(H, x.device, workspace)
-    _lib.call("s4_layernorm_channels_backward", _ptr(dz), _ptr(x), _ptr(gamma), float(eps), Bt, H, L, _ptr(dx),
-              _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace.numel(), _stream())
+    shape = x.shape
+    Bt, H, L = shape
+    xp, zp = _full(x, "x", shape, _F32, dev), _full(dz, "dz", shape, _F32, dev)
+    gp = _full(gamma, "gamma", (H,), _F32, dev)
+    dx = _out(dx, "dx", shape, _F32, dev)
+    dgamma, dbeta = _out(dgamma, "dgamma", (H,), _F32, dev), _out(dbeta, "dbeta", (H,), _F32, dev)
+    workspace = _scratch(workspace, layernorm_backward_workspace_size(H), dev)
+    _lib.call("s4_layernorm_channels_backward", zp, xp, gp, eps, Bt, H, L, dx.data_ptr(), dgamma.data_ptr(),
+              dbeta.data_ptr(), workspace.data_ptr(), workspace.numel(), _current_stream(dev))
     return dx, dgamma, dbeta
 
 
-def _tokens(t, name, dtype):
-    """[Bt, T, heads, d] with contiguous heads and evenly spaced tokens (a
-    contiguous tensor, or a slice of a wider projection): its token stride in
-    elements."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, but the current CUDA device is "
-                         f"cuda:{torch.cuda.current_device()} (use torch.cuda.device({t.device}))")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    Bt, T, H, d = t.shape
-    if Bt * T <= 1:
-        step = max(H * d, 1)
-    elif T > 1:
-        step = t.stride(1)
-    else:
-        step = t.stride(0)
-    even = ((d == 1 or t.stride(3) == 1) and (H == 1 or t.stride(2) == d)
-            and (T <= 1 or Bt == 1 or t.stride(0) == T * step))
-    if t.numel() and not even:
-        raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens")
-    return step if t.numel() else max(H * d, 1)
+def _token_stride(t, name, lead, dtype, dev):
+    """Elements between the tokens of t [*lead, heads, d]: contiguous heads,
+    evenly spaced tokens (a contiguous tensor, or a slice of a wider
+    projection)."""
+    _on(t, name, dtype, dev)
+    H, d = t.shape[-2:]
+    if t.is_contiguous():
+        return H * d
+    st = t.stride()
+    n = 1
+    step = None     # stride of the innermost token axis that has more than one token
+    for size, s in zip(reversed(lead), reversed(st[:-2])):
+        if size != 1:
+            if step is None:
+                step = s
+            elif s != n * step:
+                raise ValueError(f"{name} must have evenly spaced tokens")
+            n *= size
+    if n and ((d != 1 and st[-1] != 1) or (H != 1 and st[-2] != d)):
+        raise ValueError(f"{name} must have contiguous heads")
+    return H * d if step is None or n == 0 else step
 
 
-def _delta_args(q, k, v, g, beta):
-    """Shapes and token strides of the gated delta rule's operands."""
-    kind = _dtype(v, "v")
-    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
-        raise ValueError("q, k [Bt, T, Hk, Dk] and v [Bt, T, Hv, Dv] are wanted")
-    strides = [_tokens(t, n, v.dtype) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
-    Bt, T, Hk, Dk = q.shape
-    Hv, Dv = v.shape[2:]
-    if tuple(k.shape) != (Bt, T, Hk, Dk) or tuple(v.shape[:2]) != (Bt, T):
+def _delta_args(q, k, v, g, beta, tokens):
+    """Operands of the gated delta rule with `tokens` token axes, checked:
+    kind, device, addresses and token strides, sizes."""
+    kind, dev = _kind(v, "v"), _current_device()
+    if q.dim() != tokens + 2 or v.dim() != tokens + 2:
+        raise ValueError("q, k [Bt, T, Hk, Dk] and v [Bt, T, Hv, Dv] are wanted ([Bt, H, D] for one step)")
+    lead, (Hk, Dk), (Hv, Dv) = q.shape[:-2], q.shape[-2:], v.shape[-2:]
+    if k.shape != q.shape or v.shape[:-2] != lead:
         raise ValueError("shape mismatch between q, k and v")
-    for t, n in ((g, "g"), (beta, "beta")):
-        _buffer(_cuda(t, n), n, (Bt, T, Hv), torch.float32, v.device)
-    return kind, strides, (Bt, T, Hk, Hv, Dk, Dv)
+    dtype = v.dtype
+    ptrs = []
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        ptrs += (t.data_ptr(), _token_stride(t, n, lead, dtype, dev))
+    gates = (*lead, Hv)
+    ptrs += (_full(g, "g", gates, _F32, dev), _full(beta, "beta", gates, _F32, dev))
+    return kind, dev, ptrs, lead, (Hk, Hv, Dk, Dv)
+
+
+def _delta_scan(q, k, v, g, beta, state, scale, out, tokens):
+    kind, dev, ptrs, lead, (Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta, tokens)
+    Bt, T = lead if tokens == 2 else (lead[0], 1)
+    sp = _full(state, "state", (Bt, Hv, Dk, Dv), _F32, dev)
+    out = _out(out, "out", v.shape, v.dtype, dev)
+    _lib.call("s4_gated_delta_scan", kind, *ptrs, Dk ** -0.5 if scale is None else scale, sp, Bt, T, Hk, Hv, Dk, Dv,
+              out.data_ptr(), _current_stream(dev))
+    return out
 
 
 def gated_delta_scan(q, k, v, g, beta, state, *, scale=None, out=None):
@@ -728,22 +781,13 @@ def gated_delta_scan(q, k, v, g, beta, state, *, scale=None, out=None):
     [Bt, T, Hk, Dk], v [Bt, T, Hv, Dv] (float32, bfloat16 or float16), g, beta
     [Bt, T, Hv] and state [Bt, Hv, Dk, Dv] float32. The state is updated in
     place; returns o [Bt, T, Hv, Dv]. scale is Dk ** -0.5 by default."""
-    kind, (sq, sk, sv), (Bt, T, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
-    _buffer(_cuda(state, "state"), "state", (Bt, Hv, Dk, Dv), torch.float32, v.device)
-    out = _buffer(out, "out", v.shape, v.dtype, v.device)
-    scale = Dk ** -0.5 if scale is None else scale
-    _lib.call("s4_gated_delta_scan", kind, _ptr(q), sq, _ptr(k), sk, _ptr(v), sv, _ptr(g), _ptr(beta), float(scale),
-              _ptr(state), Bt, T, Hk, Hv, Dk, Dv, _ptr(out), _stream())
-    return out
+    return _delta_scan(q, k, v, g, beta, state, scale, out, 2)
 
 
 def gated_delta_step(q, k, v, g, beta, state, *, scale=None, out=None):
     """One token of gated_delta_scan: q, k [Bt, Hk, Dk], v [Bt, Hv, Dv], g,
     beta [Bt, Hv]; returns o [Bt, Hv, Dv]."""
-    if out is not None:
-        _cuda(out, "out")
-        out = out.unsqueeze(1)
-    return gated_delta_scan(*(t.unsqueeze(1) for t in (q, k, v, g, beta)), state, scale=scale, out=out).squeeze(1)
+    return _delta_scan(q, k, v, g, beta, state, scale, out, 1)
 
 
 def gated_delta_workspace_size(dtype, Bt, tokens, Hk, Hv, Dk, Dv, keep=False) -> int:
@@ -758,13 +802,13 @@ def gated_delta_workspace_size(dtype, Bt, tokens, Hk, Hv, Dk, Dv, keep=False) ->
     return n.value
 
 
-def _sequences(cu_seqlens, Bt):
+def _sequences(cu_seqlens, Bt, dev):
+    """How many sequences, and the address of their offsets."""
     if cu_seqlens is None:
-        return Bt
-    _cuda(cu_seqlens, "cu_seqlens", torch.int32)
+        return Bt, None
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or Bt != 1:
         raise ValueError("cu_seqlens is [N + 1] for N >= 1 sequences packed in [1, T, ...]")
-    return cu_seqlens.numel() - 1
+    return cu_seqlens.numel() - 1, _full(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, dev)
 
 
 def gated_delta_forward(q, k, v, g, beta, *, scale=None, initial_state=None, cu_seqlens=None, keep=False, out=None,
@@ -775,21 +819,22 @@ def gated_delta_forward(q, k, v, g, beta, *, scale=None, initial_state=None, cu_
     cu_seqlens (int32, [N + 1]) N sequences packed in [1, T, ...].
     initial_state [N, Hv, Dk, Dv] float32 (zeros by default; final_state may be
     the same tensor). Returns (o, final_state, workspace); with keep the
-    workspace holds what gated_delta_backward needs."""
-    kind, (sq, sk, sv), (Bt, T, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
-    n, dev = _sequences(cu_seqlens, Bt), v.device
-    if initial_state is not None:
-        _buffer(_cuda(initial_state, "initial_state"), "initial_state", (n, Hv, Dk, Dv), torch.float32, dev)
-    out = _buffer(out, "out", v.shape, v.dtype, dev)
-    final_state = _buffer(final_state, "final_state", (n, Hv, Dk, Dv), torch.float32, dev)
+    workspace holds what gated_delta_backward needs. Rows of o that no packed
+    sequence covers are left as they were (zeros in a new o)."""
+    kind, dev, ptrs, (Bt, T), (Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta, 2)
+    n, cp = _sequences(cu_seqlens, Bt, dev)
+    states = (n, Hv, Dk, Dv)
+    ip = None if initial_state is None else _full(initial_state, "initial_state", states, _F32, dev)
+    if out is None and cp is not None:
+        out = torch.zeros(v.shape, dtype=v.dtype, device="cuda")
+    out = _out(out, "out", v.shape, v.dtype, dev)
+    final_state = _out(final_state, "final_state", states, _F32, dev)
     if workspace is None:
-        need = gated_delta_workspace_size(v.dtype, n, Bt * T, Hk, Hv, Dk, Dv, keep)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _cuda(workspace, "workspace", torch.uint8)
-    scale = Dk ** -0.5 if scale is None else scale
-    _lib.call("s4_gated_delta_forward", kind, _ptr(q), sq, _ptr(k), sk, _ptr(v), sv, _ptr(g), _ptr(beta),
-              float(scale), _ptr(initial_state), _ptr(cu_seqlens), n, Bt * T, Hk, Hv, Dk, Dv, _ptr(out),
-              _ptr(final_state), int(bool(keep)), _ptr(workspace), workspace.numel(), _flags_ptr(flags), _stream())
+        workspace = _scratch(None, gated_delta_workspace_size(v.dtype, n, Bt * T, Hk, Hv, Dk, Dv, keep), dev)
+    workspace = _scratch(workspace, 0, dev)
+    _lib.call("s4_gated_delta_forward", kind, *ptrs, Dk ** -0.5 if scale is None else scale, ip, cp, n, Bt * T, Hk, Hv,
+              Dk, Dv, out.data_ptr(), final_state.data_ptr(), 1 if keep else 0, workspace.data_ptr(),
+              workspace.numel(), _flag_word(flags, dev), _current_stream(dev))
     return out, final_state, workspace
 
 
@@ -798,21 +843,19 @@ def gated_delta_backward(q, k, v, g, beta, do, workspace, *, scale=None, dfinal_
     """Gradients of gated_delta_forward (s4_gated_delta_backward): do like o,
     dfinal_state [N, Hv, Dk, Dv] (zeros by default), workspace the one that
     gated_delta_forward(..., keep=True) of the same inputs returned. Returns
-    dict(q, k, v of their type, contiguous; g, beta, initial_state float32)."""
-    kind, _, (Bt, T, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
-    n, dev = _sequences(cu_seqlens, Bt), v.device
-    _buffer(_cuda(do, "do"), "do", v.shape, v.dtype, dev)
-    if dfinal_state is not None:
-        _buffer(_cuda(dfinal_state, "dfinal_state"), "dfinal_state", (n, Hv, Dk, Dv), torch.float32, dev)
-    _cuda(workspace, "workspace", torch.uint8)
-    # rows that no packed sequence covers get no gradient
-    new = torch.empty if cu_seqlens is None else torch.zeros
-    out = {"q": new(q.shape, dtype=q.dtype, device=dev), "k": new(k.shape, dtype=k.dtype, device=dev),
-           "v": new(v.shape, dtype=v.dtype, device=dev), "g": new(g.shape, dtype=g.dtype, device=dev),
-           "beta": new(g.shape, dtype=g.dtype, device=dev),
-           "initial_state": torch.empty(n, Hv, Dk, Dv, dtype=torch.float32, device=dev)}
-    scale = Dk ** -0.5 if scale is None else scale
-    _lib.call("s4_gated_delta_backward", kind, _ptr(g), _ptr(beta), float(scale), _ptr(cu_seqlens), n, Bt * T, Hk, Hv,
-              Dk, Dv, _ptr(do), _ptr(dfinal_state), *(_ptr(out[m]) for m in ("q", "k", "v", "g", "beta", "initial_state")),
-              _ptr(workspace), workspace.numel(), _flags_ptr(flags), _stream())
+    dict(q, k, v of their type, contiguous; g, beta, initial_state float32);
+    rows that no packed sequence covers are zero."""
+    kind, dev, ptrs, (Bt, T), (Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta, 2)
+    n, cp = _sequences(cu_seqlens, Bt, dev)
+    states = (n, Hv, Dk, Dv)
+    op = _full(do, "do", v.shape, v.dtype, dev)
+    fp = None if dfinal_state is None else _full(dfinal_state, "dfinal_state", states, _F32, dev)
+    _scratch(workspace, 0, dev) if workspace is not None else _on(None, "workspace", torch.uint8, dev)
+    new = torch.empty if cp is None else torch.zeros
+    out = {m: new(t.shape, dtype=t.dtype, device="cuda")
+           for m, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta))}
+    out["initial_state"] = torch.empty(states, dtype=_F32, device="cuda")
+    _lib.call("s4_gated_delta_backward", kind, *ptrs[6:], Dk ** -0.5 if scale is None else scale, cp, n, Bt * T, Hk,
+              Hv, Dk, Dv, op, fp, *(t.data_ptr() for t in out.values()), workspace.data_ptr(), workspace.numel(),
+              _flag_word(flags, dev), _current_stream(dev))
     return out

@@ -323,7 +323,8 @@ template <typename T, int DKT>
 cudaError_t run(const DeltaArgs &a, const void *dout, const float *dlast, float *dinit, const void *ws, void *dv,
                 float *keep_ds, float *keep_dr, unsigned *flags, cudaStream_t st) {
     const int smem = Stage<T, DKT>::count(a.dv) * Stage<T, DKT>::bytes(a.dv) + 256;
-    cudaError_t e = cudaFuncSetAttribute(k_delta_backward<T, DKT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(k_delta_backward<T, DKT>, smem);
     if (e != cudaSuccess) return e;
     const unsigned char *units = (const unsigned char *)ws;
     k_delta_backward<T, DKT><<<a.n * a.hv, kThreads, smem, st>>>(

@@ -335,7 +335,8 @@ template <typename T, int DKT>
 cudaError_t run(const DeltaArgs &a, const float *init, float *last, const void *ws, float *keep_s, float *keep_e,
                 unsigned *flags, cudaStream_t st) {
     const int smem = Stage<T, DKT>::count(a.dv) * Stage<T, DKT>::bytes(a.dv) + 256;
-    cudaError_t e = cudaFuncSetAttribute(k_delta_forward<T, DKT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(k_delta_forward<T, DKT>, smem);
     if (e != cudaSuccess) return e;
     const unsigned char *units = (const unsigned char *)ws;
     k_delta_forward<T, DKT><<<a.n * a.hv, kThreads, smem, st>>>(

@@ -468,7 +468,8 @@ cudaError_t run(const DeltaArgs &a, const void *dout, const void *ws, const floa
                 const float *keep_ds, const float *keep_dr, void *dq, void *dk, float *dg, float *dbeta,
                 unsigned *flags, cudaStream_t st) {
     constexpr int smem = GradSmem<T, DKT, DVT>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(k_delta_gradient<T, DKT, DVT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(k_delta_gradient<T, DKT, DVT>, smem);
     if (e != cudaSuccess) return e;
     const long long n = slots(a.tokens, a.n);
     k_delta_gradient<T, DKT, DVT><<<(unsigned)(n * a.hk), kGradThreads, smem, st>>>(

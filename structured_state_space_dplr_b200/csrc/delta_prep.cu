@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
         *reinterpret_cast<float2 *>(fac + kC + j) =
             make_float2(b0 * exp2f((float)(all - x)), b1 * exp2f((float)(all - y)));
     }
+    umma::cp_async_commit();
     umma::cp_async_wait_all();
     umma::fence_proxy_async();
     umma::fence_before_sync();
@@ -319,7 +320,8 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
 template <typename T, int DKT>
 cudaError_t run(const DeltaArgs &a, void *ws, unsigned *flags, cudaStream_t st) {
     constexpr int smem = PrepSmem<T, DKT>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(k_delta_prep<T, DKT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(k_delta_prep<T, DKT>, smem);
     if (e != cudaSuccess) return e;
     const long long units = slots(a.tokens, a.n) * a.hv;
     k_delta_prep<T, DKT><<<(unsigned)units, 256, smem, st>>>(a, (unsigned char *)ws,

@@ -820,13 +820,11 @@ def gated_delta_forward(q, k, v, g, beta, *, scale=None, initial_state=None, cu_
     initial_state [N, Hv, Dk, Dv] float32 (zeros by default; final_state may be
     the same tensor). Returns (o, final_state, workspace); with keep the
     workspace holds what gated_delta_backward needs. Rows of o that no packed
-    sequence covers are left as they were (zeros in a new o)."""
+    sequence covers are left as they were (undefined in a new o)."""
     kind, dev, ptrs, (Bt, T), (Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta, 2)
     n, cp = _sequences(cu_seqlens, Bt, dev)
     states = (n, Hv, Dk, Dv)
     ip = None if initial_state is None else _full(initial_state, "initial_state", states, _F32, dev)
-    if out is None and cp is not None:
-        out = torch.zeros(v.shape, dtype=v.dtype, device="cuda")
     out = _out(out, "out", v.shape, v.dtype, dev)
     final_state = _out(final_state, "final_state", states, _F32, dev)
     if workspace is None:

@@ -76,9 +76,11 @@ double span(int dtype, double tokens, long long stride, long long row) {
 }
 
 // the workspace of the chunked form: units of T and PT and factors, then (keep)
-// the states before the chunks, E, the states' gradients behind the chunks and dR
+// the states before the chunks, E, the states' gradients behind the chunks and
+// dR, then the segments' summaries
 struct DeltaWork {
-    size_t state, rows, prep, total;   // bytes of one kind
+    size_t state, rows, prep, sums, total;   // bytes of one kind
+    int seg;
 };
 DeltaWork delta_work(int dtype, int Bt, long long tokens, int Hk, int Hv, int Dk, int Dv, int keep) {
     DeltaWork w;
@@ -86,7 +88,9 @@ DeltaWork delta_work(int dtype, int Bt, long long tokens, int Hk, int Hv, int Dk
     w.prep = s4::delta_prep_bytes(dtype, tokens, Bt, Hk, Hv, Dk);
     w.state = keep ? (size_t)units * Dk * Dv * 4 : 0;
     w.rows = keep ? (size_t)units * 64 * Dv * 4 : 0;
-    w.total = w.prep + 2 * w.state + 2 * w.rows;
+    w.seg = s4::delta_segment(tokens, Bt, Hv);
+    w.sums = s4::delta_segment_bytes(tokens, Bt, Hv, Dk, Dv, w.seg);
+    w.total = w.prep + 2 * w.state + 2 * w.rows + w.sums;
     return w;
 }
 
@@ -187,7 +191,7 @@ s4_status s4_gated_delta_scan(s4_dtype dtype, const void *q, long long q_stride,
                      {state, 4.0 * Bt * Hv * Dk * Dv, true},
                      {o, span(dtype, tok, (long long)Hv * Dv, (long long)Hv * Dv), true}}))
         return S4_ERR_INVALID_ARG;
-    s4::DeltaArgs a{q, k, v, g, beta, o, Bt, Hk, Hv, Dk, Dv, q_stride, k_stride, v_stride, scale, nullptr, T, Bt * (long long)T};
+    s4::DeltaArgs a{q, k, v, g, beta, o, Bt, Hk, Hv, Dk, Dv, q_stride, k_stride, v_stride, scale, nullptr, T, Bt * (long long)T, 0};
     return cuda_status(s4::launch_delta_scan(dtype, a, state, T, stream));
 }
 
@@ -229,7 +233,8 @@ s4_status s4_gated_delta_forward(s4_dtype dtype, const void *q, long long q_stri
                      {workspace, (double)workspace_bytes, true}}))
         return S4_ERR_INVALID_ARG;
     s4::DeltaArgs a{q,  k,  v,        g,        beta,     o,     Bt,         Hk,                        Hv,    Dk,
-                    Dv, q_stride, k_stride, v_stride, scale, cu_seqlens, cu_seqlens ? 0 : (int)(tokens / Bt), tokens};
+                    Dv, q_stride, k_stride, v_stride, scale, cu_seqlens, cu_seqlens ? 0 : (int)(tokens / Bt), tokens,
+                    w.seg};
     char *p = (char *)workspace;
     float *ks = keep ? (float *)(p + w.prep) : nullptr, *ke = keep ? (float *)(p + w.prep + w.state) : nullptr;
     if (tokens > 0) {
@@ -237,7 +242,8 @@ s4_status s4_gated_delta_forward(s4_dtype dtype, const void *q, long long q_stri
         if (s != S4_OK) return s;
     }
     return cuda_status(
-        s4::launch_delta_forward(dtype, a, initial_state, final_state, workspace, ks, ke, d_flags, stream));
+        s4::launch_delta_forward(dtype, a, initial_state, final_state, workspace, ks, ke,
+                                 p + w.prep + 2 * w.state + 2 * w.rows, d_flags, stream));
 }
 
 s4_status s4_gated_delta_backward(s4_dtype dtype, const float *g, const float *beta, float scale,

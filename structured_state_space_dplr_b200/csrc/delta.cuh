@@ -87,6 +87,43 @@ __device__ __forceinline__ Seq sequence(const DeltaArgs &a, int s) {
     r.slot0 = r.tok0 / kC + s;
     return r;
 }
+// Segments: a.seg chunks of one sequence (the last one fewer), or the whole
+// sequence; every sequence has one at least. Numbered like the slots.
+__host__ __device__ inline long long segments(long long slots, int n, int seg) { return (seg ? slots / seg : 0) + n; }
+struct Segment {
+    int s, index;            // sequence (-1: no such segment), number in it
+    int first, chunks;       // first chunk and chunks (none of an empty sequence)
+    bool last;               // the sequence's last
+};
+__device__ __forceinline__ long long segment0(const DeltaArgs &a, int s) {
+    return (a.seg ? sequence(a, s).slot0 / a.seg : 0) + s;
+}
+__device__ __forceinline__ Segment segment_of(const DeltaArgs &a, long long number) {
+    Segment r;
+    r.s = 0;
+    if (a.seg == 0) {
+        r.s = (int)number;
+    } else {
+        for (int lo = 0, hi = a.n; lo < hi;) {
+            const int m = (lo + hi) >> 1;
+            if (segment0(a, m) <= number) {
+                r.s = m;
+                lo = m + 1;
+            } else {
+                hi = m;
+            }
+        }
+    }
+    const int all = (sequence(a, r.s).len + kC - 1) / kC, len = a.seg ? a.seg : all;
+    const long long index = a.seg ? number - segment0(a, r.s) : 0;
+    if (index < 0 || (index > 0 && index * len >= all)) r.s = -1;
+    r.index = (int)index;
+    r.first = r.index * len;
+    r.chunks = all - r.first < len ? all - r.first : len;
+    r.last = r.first + r.chunks >= all;
+    return r;
+}
+
 // the chunk that owns a slot: its first token and its tokens (0: none)
 struct Chunk {
     long long tok;

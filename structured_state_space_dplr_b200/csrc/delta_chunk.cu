@@ -20,6 +20,8 @@
 #include "delta.cuh"
 #include "s4dplr.h"
 
+#include <cmath>
+
 namespace s4 {
 namespace {
 
@@ -36,8 +38,13 @@ constexpr int kTmS = 0, kTmSl = 128, kTmK = 192, kTmE = 256, kTmQ = 320, kTmO = 
 
 enum { bFull = 0, bEmpty = 2, bS = 4, bR = 8, bE = 10, bO = 12, bM1, bM2, bMq, bM2o, bM3, bCount };
 
-template <typename T, int DKT>
+// SUM: what a segment does to the state, S -> M S + N, without output: blocks
+// 2 b write N (the segment from a zero state), blocks 2 b + 1 M (without V,
+// from the identity; lanes are M's columns). Otherwise the segment itself, from
+// the state that `starts` has for it.
+template <typename T, int DKT, bool SUM>
 __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, const float *init, float *last,
+                                                               float *sums, const float *starts,
                                                                const unsigned char *ws,
                                                                const unsigned char *images, float *keep_s,
                                                                float *keep_e, unsigned *flags) {
@@ -48,9 +55,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + ST * stage_bytes);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + bCount);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-    const int hv = blockIdx.x % a.hv, s = blockIdx.x / a.hv, hk = hv / (a.hv / a.hk);
-    const Seq sq = sequence(a, s);
-    const int chunks = uniform((sq.len + kC - 1) / kC);
+    const unsigned block = SUM ? blockIdx.x >> 1 : blockIdx.x;
+    const bool ident = SUM && (blockIdx.x & 1);
+    const int hv = block % a.hv, hk = hv / (a.hv / a.hk);
+    const Segment sg = segment_of(a, block / a.hv);
+    if (sg.s < 0 || (SUM && sg.last)) return;
+    Seq sq = sequence(a, sg.s);   // from here on the segment as a sequence
+    sq.tok0 += (long long)sg.first * kC;
+    sq.slot0 += sg.first;
+    sq.len = sq.len - sg.first * kC < sg.chunks * kC ? sq.len - sg.first * kC : sg.chunks * kC;
+    const int chunks = uniform(sg.chunks);
+    const int dv = ident ? a.dk : a.dv;   // lanes in use
 
     if (warp == 0) umma::tmem_alloc(tslot, 512);
     if (tid == 0) {
@@ -141,12 +156,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 }
                 __syncwarp();
             }
-            ok = ok && (c == 0 || umma::mbar_wait(bars + bO, pc ^ 1, kSpinLimit));   // the last output's terms have been read
-            umma::fence_after_sync();
-            if (ok && elect())
+            if constexpr (!SUM) {
+                ok = ok && (c == 0 || umma::mbar_wait(bars + bO, pc ^ 1, kSpinLimit));   // the last output's terms have been read
+                umma::fence_after_sync();
+                if (ok && elect())
 #pragma unroll
-                for (int n = 0; n < NS / 2; ++n) state_times(kTmQ, kC, n);
-            __syncwarp();
+                    for (int n = 0; n < NS / 2; ++n) state_times(kTmQ, kC, n);
+                __syncwarp();
+            }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 ok = ok && umma::mbar_wait(bars + bR + n, pc, kSpinLimit);
@@ -155,8 +172,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                     r_times(kTmE, 0, n);
                     if (n == 1) {
                         umma::commit(bars + bM2);
+                        if constexpr (!SUM) {
 #pragma unroll
-                        for (int i = NS / 2; i < NS; ++i) state_times(kTmQ, kC, i);
+                            for (int i = NS / 2; i < NS; ++i) state_times(kTmQ, kC, i);
+                        }
                         umma::commit(bars + bMq);
                     }
                 }
@@ -183,8 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                             }
                     if (n == 1) {
                         umma::commit(bars + bM3);
-                        r_times(kTmO, 1, 0);
-                        r_times(kTmO, 1, 1);
+                        if constexpr (!SUM) {
+                            r_times(kTmO, 1, 0);
+                            r_times(kTmO, 1, 1);
+                        }
                         umma::commit(bars + bM2o);
                         umma::commit(bars + bEmpty + st);
                     }
@@ -200,14 +221,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
         // ------------------------------------------------- element-wise ----
         const int h = warp >> 2, v = (warp & 3) * 32 + lane;   // half of the columns, value channel
         const uint32_t mine = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        const bool vin = v < a.dv;
+        const bool vin = v < dv;
         const long long orow = (long long)a.hv * a.dv;
         float S[HC];
-        const size_t st0 = ((size_t)s * a.hv + hv) * a.dk * a.dv + v;
+        const size_t st0 = ((size_t)sg.s * a.hv + hv) * a.dk * a.dv + v;
+        const float *from = a.seg ? starts + (size_t)block * a.dk * a.dv + v : init ? init + st0 : nullptr;
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
             const int d = h * HC + i;
-            S[i] = init && vin && d < a.dk ? __ldg(init + st0 + (size_t)d * a.dv) : 0.0f;
+            if (SUM)
+                S[i] = ident && d == v && vin ? 1.0f : 0.0f;
+            else
+                S[i] = from && vin && d < a.dk ? __ldg(from + (size_t)d * a.dv) : 0.0f;
         }
         auto done = [&](int bar) {   // this warp's tensor-memory writes (and reads) before the barrier
             tm_wait_st();
@@ -251,16 +276,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
             }
         };
         if (chunks) put_state();
-        int before = 0;
+        [[maybe_unused]] int before = 0;
         for (int c = 0, st = 0, turn = 0; c < chunks; ++c) {
             const int pc = c & 1;
             const unsigned char *sp = smem + st * stage_bytes;
             const float *eg = reinterpret_cast<const float *>(sp + L::kTp + kTpBytes);
             // lanes past dv compute what channel 0 would be; nothing of it is stored
-            const T *vs = reinterpret_cast<const T *>(sp + L::kV) + (vin ? v : 0);
+            const T *vs = reinterpret_cast<const T *>(sp + L::kV) + (v < a.dv ? v : 0);
             const long long unit = (sq.slot0 + c) * a.hv + hv;
-            if (keep_s && vin) store_state<HC>(keep_s + (size_t)unit * a.dk * a.dv, S, h, v, a.dk, a.dv);
-            if (c > 0) put_output(c - 1, before);
+            if (!SUM && keep_s && vin) store_state<HC>(keep_s + (size_t)unit * a.dk * a.dv, S, h, v, a.dk, a.dv);
+            if (!SUM && c > 0) put_output(c - 1, before);
             ok = ok && umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit) &&
                  umma::mbar_wait(bars + bM1, pc, kSpinLimit);
             if (!ok) break;
@@ -271,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 float x[16], e[16], r[16];
                 get16(eg + j0, e);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) r[j] = to_f(vs[(j0 + j) * a.dv]);
+                for (int j = 0; j < 16; ++j) r[j] = ident ? 0.0f : to_f(vs[(j0 + j) * a.dv]);
                 tm_ld16(mine + kTmK + j0, x);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) x[j] = fmaf(-e[j], x[j], r[j]);
@@ -287,13 +312,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 float x[16], e[16];
                 get16(eg + kC + j0, e);
                 tm_ld16(mine + kTmE + j0, x);
-                if (keep_e && vin) store_tokens(keep_e + (size_t)unit * kC * a.dv, x, j0, v);
+                if (!SUM && keep_e && vin) store_tokens(keep_e + (size_t)unit * kC * a.dv, x, j0, v);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) x[j] *= e[j];
                 tm_split16(mine + kTmE + j0, mine + kTmEl + j0 / 2, x);
                 done(bE + n);
             }
             const float total = eg[kC - 1];   // e^(G_C): rows past the end have g = 0
+            if (SUM) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + bEmpty + st);
+            }
             ok = umma::mbar_wait(bars + bM3, pc, kSpinLimit);
             if (!ok) break;
             umma::fence_after_sync();
@@ -311,11 +340,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 ++turn;
             }
         }
-        if (ok && chunks) put_output(chunks - 1, before);
-        if (last && vin) {
+        if constexpr (SUM) {
+            // N [dk][dv], then M by columns [dk][dk]
+            float *to = sums + (size_t)block * a.dk * (a.dv + a.dk) + (ident ? a.dk * a.dv + v * a.dk : v);
+            if (vin)
 #pragma unroll
-            for (int i = 0; i < HC; ++i)
-                if (h * HC + i < a.dk) last[st0 + (size_t)(h * HC + i) * a.dv] = S[i];
+                for (int i = 0; i < HC; ++i)
+                    if (h * HC + i < a.dk) to[(size_t)(h * HC + i) * (ident ? 1 : a.dv)] = S[i];
+        } else {
+            if (ok && chunks) put_output(chunks - 1, before);
+            if (last && sg.last && vin) {
+#pragma unroll
+                for (int i = 0; i < HC; ++i)
+                    if (h * HC + i < a.dk) last[st0 + (size_t)(h * HC + i) * a.dv] = S[i];
+            }
         }
     }
     if (!ok && flags && lane == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
@@ -331,32 +369,117 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
     if (warp == 0) umma::tmem_dealloc(tm, 512);
 }
 
+// The states before the segments: S <- M S + N from segment to segment. A block
+// has 16 columns of one sequence's and head's state in shared memory, a thread
+// one row of the result and 8 of the columns; M is read by columns from L2.
+constexpr int kJoinCols = 16;
+__global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, const float *init, const float *sums, float *starts) {
+    __shared__ float S[128][kJoinCols];
+    const int hv = blockIdx.x % a.hv, s = blockIdx.x / a.hv, v0 = blockIdx.y * kJoinCols;
+    const int d = threadIdx.x & 127, c0 = (threadIdx.x >> 7) * 8;
+    const int all = (sequence(a, s).len + kC - 1) / kC, n = (all + a.seg - 1) / a.seg;
+    const long long first = segment0(a, s);
+    const bool in = d < a.dk && v0 + c0 < a.dv;   // dv is a multiple of 8
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        x[j] = in && init ? __ldg(init + (((size_t)s * a.hv + hv) * a.dk + d) * a.dv + v0 + c0 + j) : 0.0f;
+    for (int g = 0;; ++g) {
+        const size_t unit = (size_t)(first + g) * a.hv + hv;
+        if (in) {
+            float4 *to = reinterpret_cast<float4 *>(starts + (unit * a.dk + d) * a.dv + v0 + c0);
+            to[0] = make_float4(x[0], x[1], x[2], x[3]);
+            to[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+        if (g + 1 >= n) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) S[d][c0 + j] = x[j];
+        __syncthreads();
+        const float *N = sums + unit * a.dk * (a.dv + a.dk), *M = N + (size_t)a.dk * a.dv;
+        if (in) {
+            const float4 *np = reinterpret_cast<const float4 *>(N + (size_t)d * a.dv + v0 + c0);
+            const float4 p = __ldg(np), q = __ldg(np + 1);
+            x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
+#pragma unroll 8
+            for (int c = 0; c < a.dk; ++c) {
+                const float m = __ldg(M + (size_t)c * a.dk + d);
+                const float4 u = *reinterpret_cast<const float4 *>(&S[c][c0]);
+                const float4 w = *reinterpret_cast<const float4 *>(&S[c][c0 + 4]);
+                x[0] = fmaf(m, u.x, x[0]);
+                x[1] = fmaf(m, u.y, x[1]);
+                x[2] = fmaf(m, u.z, x[2]);
+                x[3] = fmaf(m, u.w, x[3]);
+                x[4] = fmaf(m, w.x, x[4]);
+                x[5] = fmaf(m, w.y, x[5]);
+                x[6] = fmaf(m, w.z, x[6]);
+                x[7] = fmaf(m, w.w, x[7]);
+            }
+        }
+        __syncthreads();
+    }
+}
+
 template <typename T, int DKT>
 cudaError_t run(const DeltaArgs &a, const float *init, float *last, const void *ws, float *keep_s, float *keep_e,
-                unsigned *flags, cudaStream_t st) {
+                void *summaries, unsigned *flags, cudaStream_t st) {
     const int smem = Stage<T, DKT>::count(a.dv) * Stage<T, DKT>::bytes(a.dv) + 256;
-    static SmemLimit limit;
-    cudaError_t e = limit.raise(k_delta_forward<T, DKT>, smem);
+    static SmemLimit limit, limit_sum;
+    cudaError_t e = limit.raise(k_delta_forward<T, DKT, false>, smem);
     if (e != cudaSuccess) return e;
-    const unsigned char *units = (const unsigned char *)ws;
-    k_delta_forward<T, DKT><<<a.n * a.hv, kThreads, smem, st>>>(
-        a, init, last, units, units + (size_t)slots(a.tokens, a.n) * a.hv * kUnitBytes, keep_s, keep_e, flags);
+    const long long chunks = slots(a.tokens, a.n), blocks = segments(chunks, a.n, a.seg) * a.hv;
+    const unsigned char *units = (const unsigned char *)ws, *images = units + (size_t)chunks * a.hv * kUnitBytes;
+    float *sums = (float *)summaries, *starts = sums + (size_t)blocks * a.dk * (a.dk + a.dv);
+    if (a.seg) {
+        e = limit_sum.raise(k_delta_forward<T, DKT, true>, smem);
+        if (e != cudaSuccess) return e;
+        k_delta_forward<T, DKT, true><<<(unsigned)(2 * blocks), kThreads, smem, st>>>(a, init, nullptr, sums, nullptr, units,
+                                                                                    images, nullptr, nullptr, flags);
+        k_delta_join<<<dim3(a.n * a.hv, (a.dv + kJoinCols - 1) / kJoinCols), 256, 0, st>>>(a, init, sums, starts);
+    }
+    k_delta_forward<T, DKT, false><<<(unsigned)blocks, kThreads, smem, st>>>(a, init, last, nullptr, starts, units, images,
+                                                                            keep_s, keep_e, flags);
     return cudaGetLastError();
 }
 
 }  // namespace
 
+// Few long chains leave most SMs idle: then every sequence is cut into segments,
+// what each does to the state is computed for all at once (twice the chain's
+// work: M and N), joined, and the segments run again from their states. Times
+// in chunks of a chain (2.9 us; M and N without output 0.85 of that, a join
+// 1.5, the extra launches 4), for sequences of average length. One sequence of
+// 65536 tokens, 8 heads of 128: 3515 us in one piece.
+int delta_segment(long long tokens, int n, int hv) {
+    constexpr double kSms = 148;
+    const double chains = (double)n * hv, c = ceil((double)tokens / kC / n);
+    double best = 0.9 * ceil(chains / kSms) * c;
+    int seg = 0;
+    for (int k = 3; k <= 64 && k <= c; ++k) {
+        const double len = ceil(c / k), t = ceil(2 * chains * (k - 1) / kSms) * len * 0.85 +
+                                            ceil(chains * k / kSms) * len + 1.5 * k + 4;
+        if (t < best) {
+            best = t;
+            seg = (int)len;
+        }
+    }
+    return seg;
+}
+
+size_t delta_segment_bytes(long long tokens, int n, int hv, int dk, int dv, int seg) {
+    return seg ? (size_t)segments(slots(tokens, n), n, seg) * hv * dk * (dk + 2 * (size_t)dv) * sizeof(float) : 0;
+}
+
 cudaError_t launch_delta_forward(int dtype, const DeltaArgs &a, const float *init, float *last, const void *ws,
-                                 float *keep_s, float *keep_e, unsigned *flags, cudaStream_t st) {
+                                 float *keep_s, float *keep_e, void *summaries, unsigned *flags, cudaStream_t st) {
     const bool wide = a.dk > 64;
     if (dtype == S4_BF16)
-        return wide ? run<__nv_bfloat16, 128>(a, init, last, ws, keep_s, keep_e, flags, st)
-                    : run<__nv_bfloat16, 64>(a, init, last, ws, keep_s, keep_e, flags, st);
+        return wide ? run<__nv_bfloat16, 128>(a, init, last, ws, keep_s, keep_e, summaries, flags, st)
+                    : run<__nv_bfloat16, 64>(a, init, last, ws, keep_s, keep_e, summaries, flags, st);
     if (dtype == S4_F16)
-        return wide ? run<__half, 128>(a, init, last, ws, keep_s, keep_e, flags, st)
-                    : run<__half, 64>(a, init, last, ws, keep_s, keep_e, flags, st);
-    return wide ? run<float, 128>(a, init, last, ws, keep_s, keep_e, flags, st)
-                : run<float, 64>(a, init, last, ws, keep_s, keep_e, flags, st);
+        return wide ? run<__half, 128>(a, init, last, ws, keep_s, keep_e, summaries, flags, st)
+                    : run<__half, 64>(a, init, last, ws, keep_s, keep_e, summaries, flags, st);
+    return wide ? run<float, 128>(a, init, last, ws, keep_s, keep_e, summaries, flags, st)
+                : run<float, 64>(a, init, last, ws, keep_s, keep_e, summaries, flags, st);
 }
 
 }  // namespace s4

@@ -105,6 +105,7 @@ struct DeltaArgs {
     const int *cu;
     int t;
     long long tokens;
+    int seg;   // chunks of a segment of a sequence; 0: sequences are not split
 };
 // T tokens for each sequence, state [n, hv, dk, dv] in place
 cudaError_t launch_delta_scan(int dtype, const DeltaArgs &a, float *state, int T, cudaStream_t st);
@@ -113,9 +114,13 @@ cudaError_t launch_delta_scan(int dtype, const DeltaArgs &a, float *state, int T
 size_t delta_prep_bytes(int dtype, long long tokens, int n, int hk, int hv, int dk);
 // the chunks' images of T and PT and the gates' factors
 cudaError_t launch_delta_prep(int dtype, const DeltaArgs &a, void *ws, unsigned *flags, cudaStream_t st);
-// o and the last states; keep_s, keep_e (or null): the state before every chunk and E of every chunk
+// o and the last states; keep_s, keep_e (or null): the state before every chunk and E of every chunk.
+// a.seg > 0: each sequence in segments, summaries: delta_segment_bytes of scratch
 cudaError_t launch_delta_forward(int dtype, const DeltaArgs &a, const float *init, float *last, const void *ws,
-                                 float *keep_s, float *keep_e, unsigned *flags, cudaStream_t st);
+                                 float *keep_s, float *keep_e, void *summaries, unsigned *flags, cudaStream_t st);
+// whether splitting pays: chunks of a segment, or 0
+int delta_segment(long long tokens, int n, int hv);
+size_t delta_segment_bytes(long long tokens, int n, int hv, int dk, int dv, int seg);
 
 // backward in the states: dV, the first states' gradient, keep_ds and keep_dr (behind every chunk, of every chunk)
 cudaError_t launch_delta_backward(int dtype, const DeltaArgs &a, const void *dout, const float *dlast, float *dinit,

@@ -62,3 +62,33 @@ def test_gated_delta_scan_rejects_bad_arguments(lib):
     assert f(sq=255) == f(sq=248) == f(sv=504) == f(sk=260) == f(scale=float("inf")) == bad
     assert f(q=p(FAKE + 8)) == f(o=v) == f(st=o) == f(o=q) == bad
     assert f(T=0, q=p(0)) == _lib.S4_OK
+
+
+def test_gated_delta_chunks_reject_bad_arguments(lib):
+    q, k, v, g, be, st, o, ws, fs, do, dq, dk, dv, dg, db = (p(FAKE + 0x10000000 * i) for i in range(15))
+    n = ctypes.c_size_t()
+    size = lambda dt=1, Bt=2, tok=200, Hk=2, Hv=4, Dk=128, Dv=128, keep=1: lib.s4_gated_delta_workspace_size(  # noqa: E731
+        dt, Bt, tok, Hk, Hv, Dk, Dv, keep, ctypes.byref(n))
+    bad, no = _lib.S4_ERR_INVALID_ARG, _lib.S4_ERR_UNSUPPORTED
+    assert size(dt=5) == size(Bt=0) == size(tok=-1) == size(Hv=3) == bad
+    assert size(Dk=12) == size(Dv=256) == size(tok=1 << 31) == size(tok=(1 << 31) - 1, Hv=128, Hk=128) == no
+    assert lib.s4_gated_delta_workspace_size(1, 2, 200, 2, 4, 128, 128, 1, None) == bad
+    assert size(keep=0) == 0
+    small = n.value
+    assert size() == 0 and n.value > small and n.value % 256 == 0
+    need = n.value
+
+    def f(dt=1, q=q, sq=256, st=st, cu=0, Bt=2, tok=200, Dk=128, o=o, fs=fs, keep=1, ws=ws, nb=need, scale=1.0):
+        return lib.s4_gated_delta_forward(dt, q, sq, k, 256, v, 512, g, be, ctypes.c_float(scale), st, p(cu), Bt, tok, 2,
+                                          4, Dk, 128, o, fs, keep, ws, nb, p(0), p(0))
+    assert f(dt=9) == f(q=p(0)) == f(o=p(0)) == f(sq=128) == f(tok=201) == f(scale=float("inf")) == bad
+    assert f(o=v) == f(fs=o) == f(o=ws) == f(st=p(FAKE + 0x50000000 + 8)) == f(fs=ws) == bad
+    assert f(Dk=130) == f(Dk=136) == no
+    assert f(ws=p(0)) == f(nb=need - 1) == f(ws=p(FAKE + 0x70000010)) == _lib.S4_ERR_WORKSPACE
+
+    def b(do=do, dq=dq, dv=dv, dg=dg, tok=200, Bt=2, ws=ws, nb=need):
+        return lib.s4_gated_delta_backward(1, g, be, ctypes.c_float(1.0), p(0), Bt, tok, 2, 4, 128, 128, do, p(0), dq, dk,
+                                           dv, dg, db, p(0), ws, nb, p(0), p(0))
+    assert b(do=p(0)) == b(dq=p(0)) == b(dg=p(0)) == b(tok=201) == b(Bt=0) == bad
+    assert b(dv=do) == b(dq=dk) == b(dg=db) == b(dv=ws) == bad
+    assert b(ws=p(0)) == b(nb=small) == _lib.S4_ERR_WORKSPACE

@@ -131,3 +131,189 @@ def test_many_blocks_at_once(dtype):
         assert all(torch.isfinite(t).all() for t in got)
         first = first or got
         assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def packed(d, cu):
+    """The oracle's arguments for sequences packed in d, with a state for each."""
+    torch = torch_cuda()
+    n, (Hv, Dk, Dv) = len(cu) - 1, d["state"].shape[1:]
+    d["state"] = 0.5 * torch.randn(n, Hv, Dk, Dv, device="cuda", generator=gen(7))
+    d["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    return [f64(d[n]) for n in NAMES]
+
+
+# offsets with sequences of no and of one token, ends inside and at the end of
+# a chunk, tokens before the first and behind the last sequence; few heads, so
+# that the longest one runs in segments
+CUS = [[0, 300], [0, 0, 1, 64, 129, 300], [5, 5, 6, 70, 198, 199], [0, 1200], [3, 3, 900, 1111, 1111], [0, 0, 0]]
+
+
+@pytest.mark.parametrize("cu", CUS)
+@pytest.mark.parametrize("dtype,shape", [("bfloat16", (2, 4, 64, 48)), ("float32", (1, 3, 72, 128))])
+def test_packed(cu, dtype, shape):
+    torch = torch_cuda()
+    import structured_state_space_dplr_b200 as s4
+    T = max(cu[-1] + 9, 20)
+    d = make(1, T, *shape, dtype=dtype)
+    args = packed(d, cu)
+    inside = torch.zeros(T, dtype=torch.bool, device="cuda")
+    inside[cu[0]:cu[-1]] = True
+    for n in NAMES:        # what lies outside the sequences is not looked at
+        d[n][:, ~inside] = float("nan")
+    do = torch.randn(d["v"].shape, device="cuda", generator=gen(1)).to(d["v"].dtype)
+    do[:, ~inside] = float("inf")
+    ds = torch.randn(d["state"].shape, device="cuda", generator=gen(2))
+    ref, last, gr = delta.gated_delta(*args, 0.5, f64(d["state"]), cu=cu, do=f64(do), dstate=f64(ds))
+    o = torch.full_like(d["v"], 7.0)
+    final = d["state"].clone()
+    _, final, work = forward(d, scale=0.5, initial_state=final, final_state=final, cu_seqlens=d["cu"], keep=True, out=o)
+    check(o, ref, o.dtype, "o")
+    check(final, last, torch.float32, "state")
+    assert (o[:, ~inside] == 7.0).all()
+    got = backward(d, do, work, scale=0.5, dfinal_state=ds, cu_seqlens=d["cu"])
+    for m in (*NAMES, "initial_state"):
+        check(got[m], gr[m], got[m].dtype, "d" + m, 2)
+        if m != "initial_state":
+            assert not got[m][:, ~inside].any()
+    for i in range(len(cu) - 1):     # an empty sequence hands its state (and the state's gradient) through
+        if cu[i] == cu[i + 1]:
+            assert torch.equal(final[i], d["state"][i]) and torch.equal(got["initial_state"][i], ds[i])
+
+
+@pytest.mark.parametrize("shape", [(1, 1500, 1, 2, 64, 64), (1, 3000, 2, 2, 128, 96), (2, 2000, 1, 1, 40, 128)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_few_long_sequences_run_in_segments(shape, dtype):
+    torch = torch_cuda()
+    import structured_state_space_dplr_b200 as s4
+    d = make(*shape, dtype=dtype)
+    d["g"] *= 0.02                  # slow decay: states reach over many segments
+    ref, last = delta.gated_delta(*(f64(d[n]) for n in NAMES), shape[4] ** -0.5, f64(d["state"]))
+    state = d["state"].clone()
+    o, got, _ = forward(d, initial_state=state, final_state=state)
+    check(o, ref, d["v"].dtype, "o", 2)       # the segments' states pass one more chain and the joins
+    check(got, last, torch.float32, "state", 2)
+    assert torch.equal(got, state)
+
+
+def test_decode_continues_prefill():
+    """norm -> projections -> prefill in chunks -> decode steps, against one pass over all tokens."""
+    torch = torch_cuda()
+    import structured_state_space_dplr_b200 as s4
+    T, more, D, Hk, Hv, Dk, Dv = 150, 5, 96, 2, 4, 64, 32
+    x = torch.randn(2, T + more, D, device="cuda", generator=gen(0)) * 2 + 1
+    gamma, beta = torch.ones(D, device="cuda"), torch.zeros(D, device="cuda")
+    z, _, _ = s4.layernorm(x, gamma, beta)
+    w = torch.randn(D, (2 * Hk * Dk + Hv * Dv), device="cuda", generator=gen(1)) / D ** 0.5
+    mixed = (z @ w).to(torch.bfloat16)
+    q, k, v = mixed.split([Hk * Dk, Hk * Dk, Hv * Dv], -1)
+    q, k, v = q.unflatten(-1, (Hk, Dk)), k.unflatten(-1, (Hk, Dk)), v.unflatten(-1, (Hv, Dv))
+    k = torch.nn.functional.normalize(k.float(), dim=-1).to(torch.bfloat16)
+    g = -torch.rand(2, T + more, Hv, device="cuda", generator=gen(2))
+    b = torch.rand(2, T + more, Hv, device="cuda", generator=gen(3))
+    whole, last, _ = s4.gated_delta_forward(q, k, v, g, b)
+    cut = lambda s: [t[:, s] for t in (q, k, v)] + [t[:, s].contiguous() for t in (g, b)]  # noqa: E731
+    pre = cut(slice(0, T))
+    with pytest.raises(ValueError):           # a cut in time of a batch is not evenly spaced
+        s4.gated_delta_forward(*pre)
+    o, state, _ = s4.gated_delta_forward(*(t.contiguous() for t in pre))
+    outs = [o]
+    for t in range(T, T + more):
+        one = [x[:, t] for x in (q, k, v)] + [x[:, t].contiguous() for x in (g, b)]
+        outs.append(s4.gated_delta_step(*one, state).unsqueeze(1))
+    check(torch.cat(outs, 1), f64(whole), torch.bfloat16, "o", 2, 2)
+    check(state, f64(last), torch.float32, "state", 2)
+
+
+def test_resets_and_values_that_are_not_finite():
+    torch = torch_cuda()
+    import structured_state_space_dplr_b200 as s4
+    d = make(1, 200, 1, 2, 64, 64)
+    d["g"][0, 70] = -float("inf")
+    d["g"][0, 130, 0] = -1e30
+    d["g"][0, 20, 1] = -300.0                 # no later difference of sums may lose what follows
+    with np.errstate(all="ignore"):
+        ref, last, gr = delta.gated_delta(*(f64(d[n]) for n in NAMES), 1.0, f64(d["state"]),
+                                          do=np.ones(d["v"].shape), dstate=np.ones(d["state"].shape))
+    o, got, work = forward(d, scale=1.0, initial_state=d["state"], keep=True)
+    check(o, ref, torch.float32, "o")
+    check(got, last, torch.float32, "state")
+    grads = backward(d, torch.ones_like(d["v"]), work, scale=1.0, dfinal_state=torch.ones_like(d["state"]))
+    for m in (*NAMES, "initial_state"):
+        check(grads[m], gr[m], torch.float32, "d" + m, 2)
+    # a NaN in one head's v stays in that head, and before it nothing changes
+    d["v"][0, 100, 1, 3] = float("nan")
+    o2, got2, _ = forward(d, scale=1.0, initial_state=d["state"])
+    assert torch.equal(o2[:, :, 0], o[:, :, 0]) and torch.equal(got2[:, 0], got[:, 0])
+    assert torch.equal(o2[:, :64, 1], o[:, :64, 1]) and torch.isnan(o2[0, 101:, 1, 3]).all()
+
+
+@pytest.mark.parametrize("scale", [1e-18, 1e18])
+def test_any_scale_of_the_values(scale):
+    """Parts have float's exponents: results scale with v and the states (by a power of two exactly)."""
+    torch = torch_cuda()
+    scale = 2.0 ** round(np.log2(scale))
+    d = make(1, 130, 1, 1, 64, 64)
+    one, last, _ = forward(d, initial_state=d["state"])
+    d["v"] *= scale
+    two, last2, _ = forward(d, initial_state=d["state"] * scale)
+    assert torch.equal(two, one * scale) and torch.equal(last2, last * scale)
+
+
+def test_strided_tokens_and_streams_and_graph():
+    torch = torch_cuda()
+    import structured_state_space_dplr_b200 as s4
+    B, T, Hk, Hv, Dk, Dv = 2, 140, 2, 4, 64, 64
+    d = make(B, T, Hk, Hv, Dk, Dv, "bfloat16")
+    do = torch.randn(d["v"].shape, device="cuda", generator=gen(1)).to(torch.bfloat16)
+    want = forward(d, initial_state=d["state"], keep=True)
+    grads = backward(d, do, want[2])
+    wide = torch.cat([d[n].flatten(2) for n in ("q", "k", "v")], -1)
+    e = dict(d)
+    for n, t, h, w in zip(("q", "k", "v"), wide.split([Hk * Dk, Hk * Dk, Hv * Dv], -1), (Hk, Hk, Hv), (Dk, Dk, Dv)):
+        e[n] = t.unflatten(-1, (h, w))
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        got = forward(e, initial_state=d["state"], keep=True)
+        g2 = backward(e, do, got[2])
+    stream.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert all(torch.equal(g2[m], grads[m]) for m in grads)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, last, work = s4.gated_delta_forward(*(d[n] for n in NAMES), initial_state=d["state"], keep=True)
+        g3 = s4.gated_delta_backward(*(d[n] for n in NAMES), do, work)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(last, want[1]) and all(torch.equal(g3[m], grads[m]) for m in grads)
+
+
+def test_refusals():
+    torch = torch_cuda()
+    import structured_state_space_dplr_b200 as s4
+    d = make(2, 70, 2, 4, 64, 64, "bfloat16")
+    args = lambda **c: [c.get(n, d[n]) for n in NAMES]  # noqa: E731
+    cu = torch.tensor([0, 70], dtype=torch.int32, device="cuda")
+    for bad, kind in [(dict(q=d["q"].float()), TypeError), (dict(g=d["g"].double()), TypeError),
+                      (dict(k=d["k"][:, :5]), ValueError), (dict(v=d["v"].cpu()), TypeError),
+                      (dict(beta=d["beta"][:, :, :2]), ValueError), (dict(q=d["q"][..., :32]), ValueError),
+                      (dict(q=d["q"].transpose(1, 2)), ValueError)]:
+        with pytest.raises(kind):
+            s4.gated_delta_forward(*args(**bad))
+    with pytest.raises(ValueError):
+        s4.gated_delta_forward(*args(), cu_seqlens=cu)                       # a batch of two cannot be packed
+    with pytest.raises(s4.S4Error):
+        s4.gated_delta_forward(*args(), workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(s4.S4Error):
+        s4.gated_delta_forward(*args(), scale=float("nan"))
+    o, last, work = s4.gated_delta_forward(*args())
+    with pytest.raises(s4.S4Error):                                          # a workspace without what backward reads
+        s4.gated_delta_backward(*args(), torch.empty_like(d["v"]), work)
+    with pytest.raises(TypeError):
+        s4.gated_delta_backward(*args(), torch.empty_like(d["v"]), None)
+    e = make(1, 8, 1, 1, 20, 64)
+    with pytest.raises(s4.S4Error):
+        s4.gated_delta_forward(*(e[n] for n in NAMES))                       # Dk not a multiple of 8
+    with pytest.raises(s4.S4Error):
+        s4.gated_delta_scan(*(e[n] for n in NAMES), e["state"])

@@ -634,11 +634,19 @@ def _full(t, name, shape, dtype, dev):
     return t.data_ptr()
 
 
-def _out(t, name, shape, dtype, dev):
-    """t, checked, or a new tensor where it is None."""
+def _out(t, name, shape, like, dev):
+    """t, checked, or a new tensor where it is None; of like's type and device."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device="cuda")
-    _full(t, name, shape, dtype, dev)
+        return like.new_empty(shape)
+    _full(t, name, shape, like.dtype, dev)
+    return t
+
+
+def _out_like(t, name, like, dev):
+    """t, checked, or a new contiguous tensor where it is None; like `like`."""
+    if t is None:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    _full(t, name, like.shape, like.dtype, dev)
     return t
 
 
@@ -669,8 +677,9 @@ def layernorm(x, gamma, beta, eps=1e-5, *, out=None, mean=None, rstd=None):
     lead, D = shape[:-1], shape[-1]
     xp = _full(x, "x", shape, dtype, dev)
     gp, bp = _full(gamma, "gamma", (D,), _F32, dev), _full(beta, "beta", (D,), _F32, dev)
-    out = _out(out, "out", shape, dtype, dev)
-    mean, rstd = _out(mean, "mean", lead, _F32, dev), _out(rstd, "rstd", lead, _F32, dev)
+    out = _out_like(out, "out", x, dev)
+    mean = _out(mean, "mean", lead, gamma, dev)
+    rstd = _out_like(rstd, "rstd", mean, dev)
     _lib.call("s4_layernorm", kind, xp, gp, bp, eps, mean.numel(), D, out.data_ptr(), mean.data_ptr(),
               rstd.data_ptr(), _current_stream(dev))
     return out, mean, rstd
@@ -698,8 +707,8 @@ def layernorm_backward(dz, x, gamma, mean, rstd, *, dx=None, dgamma=None, dbeta=
     xp, zp = _full(x, "x", shape, dtype, dev), _full(dz, "dz", shape, dtype, dev)
     gp, mp, rp = (_full(gamma, "gamma", (D,), _F32, dev), _full(mean, "mean", lead, _F32, dev),
                   _full(rstd, "rstd", lead, _F32, dev))
-    dx = _out(dx, "dx", shape, dtype, dev)
-    dgamma, dbeta = _out(dgamma, "dgamma", (D,), _F32, dev), _out(dbeta, "dbeta", (D,), _F32, dev)
+    dx = _out_like(dx, "dx", x, dev)
+    dgamma, dbeta = _out_like(dgamma, "dgamma", gamma, dev), _out_like(dbeta, "dbeta", gamma, dev)
     workspace = _scratch(workspace, layernorm_backward_workspace_size(D), dev)
     _lib.call("s4_layernorm_backward", kind, zp, xp, gp, mp, rp, mean.numel(), D, dx.data_ptr(), dgamma.data_ptr(),
               dbeta.data_ptr(), workspace.data_ptr(), workspace.numel(), _current_stream(dev))
@@ -717,8 +726,8 @@ def layernorm_channels_backward(dz, x, gamma, eps=1e-5, *, dx=None, dgamma=None,
     Bt, H, L = shape
     xp, zp = _full(x, "x", shape, _F32, dev), _full(dz, "dz", shape, _F32, dev)
     gp = _full(gamma, "gamma", (H,), _F32, dev)
-    dx = _out(dx, "dx", shape, _F32, dev)
-    dgamma, dbeta = _out(dgamma, "dgamma", (H,), _F32, dev), _out(dbeta, "dbeta", (H,), _F32, dev)
+    dx = _out_like(dx, "dx", x, dev)
+    dgamma, dbeta = _out_like(dgamma, "dgamma", gamma, dev), _out_like(dbeta, "dbeta", gamma, dev)
     workspace = _scratch(workspace, layernorm_backward_workspace_size(H), dev)
     _lib.call("s4_layernorm_channels_backward", zp, xp, gp, eps, Bt, H, L, dx.data_ptr(), dgamma.data_ptr(),
               dbeta.data_ptr(), workspace.data_ptr(), workspace.numel(), _current_stream(dev))
@@ -770,7 +779,7 @@ def _delta_scan(q, k, v, g, beta, state, scale, out, tokens):
     kind, dev, ptrs, lead, (Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta, tokens)
     Bt, T = lead if tokens == 2 else (lead[0], 1)
     sp = _full(state, "state", (Bt, Hv, Dk, Dv), _F32, dev)
-    out = _out(out, "out", v.shape, v.dtype, dev)
+    out = _out_like(out, "out", v, dev)
     _lib.call("s4_gated_delta_scan", kind, *ptrs, Dk ** -0.5 if scale is None else scale, sp, Bt, T, Hk, Hv, Dk, Dv,
               out.data_ptr(), _current_stream(dev))
     return out
@@ -825,8 +834,8 @@ def gated_delta_forward(q, k, v, g, beta, *, scale=None, initial_state=None, cu_
     n, cp = _sequences(cu_seqlens, Bt, dev)
     states = (n, Hv, Dk, Dv)
     ip = None if initial_state is None else _full(initial_state, "initial_state", states, _F32, dev)
-    out = _out(out, "out", v.shape, v.dtype, dev)
-    final_state = _out(final_state, "final_state", states, _F32, dev)
+    out = _out_like(out, "out", v, dev)
+    final_state = _out(final_state, "final_state", states, g, dev)
     if workspace is None:
         workspace = _scratch(None, gated_delta_workspace_size(v.dtype, n, Bt * T, Hk, Hv, Dk, Dv, keep), dev)
     workspace = _scratch(workspace, 0, dev)

@@ -44,21 +44,6 @@ constexpr int kFacBytes = 2 * kC * 4;          // e^G and beta e^(G_C - G)
 constexpr int kUnitBytes = kTpBytes + kFacBytes;   // workspace of one chunk and value head
 constexpr uint32_t kSpinLimit = 1u << 22;
 
-// A kernel's limit of dynamic shared memory, raised once per device (raising it
-// twice, from two threads, is harmless).
-struct SmemLimit {
-    int set[64] = {};
-    template <typename K>
-    cudaError_t raise(K *kernel, int bytes) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess || (dev < 64 && set[dev] >= bytes)) return e;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e == cudaSuccess && dev < 64) set[dev] = bytes;
-        return e;
-    }
-};
-
 // parts that an input of the type is exactly the sum of (float: to 24 bits)
 template <typename T> struct Parts { static constexpr int n = 3; };
 template <> struct Parts<__nv_bfloat16> { static constexpr int n = 1; };

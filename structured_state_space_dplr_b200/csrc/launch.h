@@ -5,6 +5,21 @@
 
 namespace s4 {
 
+// A kernel's limit of dynamic shared memory, raised once per device (raising it
+// twice, from two threads, is harmless).
+struct SmemLimit {
+    size_t set[64] = {};
+    template <typename K>
+    cudaError_t raise(K *kernel, size_t bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess || (dev < 64 && set[dev] >= bytes)) return e;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess && dev < 64) set[dev] = bytes;
+        return e;
+    }
+};
+
 // remember a failing CUDA call for s4_last_cuda_error() (calling host thread)
 void record_cuda_error(cudaError_t e);
 

@@ -14,6 +14,7 @@
 #include "dtype.cuh"
 #include "launch.h"
 #include "s4dplr.h"
+#include "umma.cuh"
 
 #include <type_traits>
 
@@ -49,65 +50,199 @@ __device__ __forceinline__ void group_sum(float (&v)[N], int tpr, float *buf, in
     }
 }
 
-template <typename T, int V, int NV, bool BIG, int MAXT>
-__global__ void __launch_bounds__(MAXT) k_layernorm_rows(const T *__restrict__ x,
-                                                                     const float *__restrict__ gamma,
-                                                                     const float *__restrict__ beta, float eps,
-                                                                     long long rows, int D, int tpr, T *z,
-                                                                     float *mean, float *rstd) {
-    __shared__ float buf[2 * 32];
-    int turn = 0;
-    const int groups = blockDim.x / tpr, l = threadIdx.x % tpr;
-    const long long row = (long long)blockIdx.x * groups + threadIdx.x / tpr;
-    const bool in = row < rows;
-    float v[NV][V];
-    float s[1] = {0.0f};
+// A thread's weights: in registers up to 16 elements, above from L1 where they
+// are used. `wide`: the array is 16-byte aligned (D is a multiple of V).
+template <int V, int NV>
+struct Weights {
+    static constexpr bool kKept = V * NV <= 16;
+    float kept[kKept ? NV : 1][V];
+    const float *w;
+    int l, tpr, D;
+    bool wide;
+    __device__ __forceinline__ Weights(const float *w_, int l_, int tpr_, int D_)
+        : w(w_), l(l_), tpr(tpr_), D(D_), wide(V >= 4 && ((size_t)w_ & 15) == 0) {
+        if constexpr (kKept)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+            for (int i = 0; i < NV; ++i) load(i, kept[i]);
+    }
+    __device__ __forceinline__ void load(int i, float (&o)[V]) const {
         const int c = (l + i * tpr) * V;
-        if (in && c < D) {
-            load_pack<T, V>(x + row * D + c, v[i]);
+        if constexpr (V >= 4) {
+            if (wide) {
+                if (c < D)
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[0] += v[i][j];
+                    for (int j = 0; j < V; j += 4) {
+                        const float4 f = __ldg(reinterpret_cast<const float4 *>(w + c + j));
+                        o[j] = f.x, o[j + 1] = f.y, o[j + 2] = f.z, o[j + 3] = f.w;
+                    }
+                return;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (c + j < D) o[j] = __ldg(w + c + j);
+    }
+    __device__ __forceinline__ void get(int i, float (&o)[V]) const {
+        if constexpr (kKept) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) o[j] = kept[i][j];
+        } else {
+            load(i, o);
         }
     }
-    group_sum<1, BIG>(s, tpr, buf, turn);
-    const float mu = s[0] / (float)D;
-    s[0] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (in && (l + i * tpr) * V < D)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[i][j] -= mu;
-                s[0] = fmaf(v[i][j], v[i][j], s[0]);
-            }
-    group_sum<1, BIG>(s, tpr, buf, turn);
-    const float rs = 1.0f / sqrtf(s[0] / (float)D + eps);
-    if (!in) return;
-    if (l == 0) {
-        mean[row] = mu;
-        rstd[row] = rs;
+};
+
+// Rows of 16-byte packs go through a ring in shared memory: kStages - 1 rounds
+// of rows are on their way while one is reduced, two rows a round where a row
+// takes one pack a thread. A thread copies exactly what it reads, so the ring
+// needs no barrier, and it reads a pack again rather than keep it: with the rows
+// in registers the loads in flight were paid for in occupancy (32768 rows of
+// 1024 bf16: forward 86 us a row a block, 49 us four rows at a time, 41 us now;
+// backward 74, 117 and 61 us; float rows reach 4.5 and 5.5 TB/s, bf16 ones are
+// bound by their instructions). Single elements (V = 1) are loaded where they are used.
+constexpr int kStages = 3;
+template <int V, int NV>
+__host__ __device__ constexpr int rows_at_once() { return V > 1 && NV <= 2 ? 2 : 1; }
+
+// ARR arrays of rows; ring [stage][row][array][NV][thread]
+template <typename T, int V, int NV, int ARR>
+struct Rows {
+    static constexpr int R = rows_at_once<V, NV>();
+    Pack<T, V> *ring;
+    const T *src[ARR];
+    long long rows;
+    int D, l, tpr, stage;
+
+    static size_t bytes(int block) { return V > 1 ? (size_t)kStages * R * ARR * NV * block * 16 : 0; }
+    __device__ __forceinline__ Pack<T, V> *slot(int st, int q, int a, int i) const {
+        return ring + (((st * R + q) * ARR + a) * NV + i) * (int)blockDim.x + threadIdx.x;
     }
+    // rows r .. r + R - 1 into stage st
+    __device__ __forceinline__ void fetch(long long r, int st) const {
+        if constexpr (V > 1) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (l + i * tpr) * V;
-        if (c < D) {
-            float o[V];
+            for (int q = 0; q < R; ++q)
+                if (r + q < rows)
 #pragma unroll
-            for (int j = 0; j < V; ++j) o[j] = fmaf(v[i][j] * rs, __ldg(gamma + c + j), __ldg(beta + c + j));
-            store_pack<T, V>(z + row * D + c, o);
+                    for (int a = 0; a < ARR; ++a)
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) {
+                            const int c = (l + i * tpr) * V;
+                            if (c < D) umma::cp_async16(slot(st, q, a, i), src[a] + (r + q) * D + c);
+                        }
+            umma::cp_async_commit();
+        }
+    }
+    // the oldest round has arrived
+    __device__ __forceinline__ void wait() const {
+        if constexpr (V > 1) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    }
+    // pack i of row r + q, array a, of the current round
+    __device__ __forceinline__ void get(long long r, int q, int a, int i, float (&o)[V]) const {
+        Pack<T, V> p;
+        if constexpr (V > 1)
+            p = *slot(stage, q, a, i);
+        else
+            p.v[0] = src[a][(r + q) * D + l + i * tpr];
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = to_f(p.v[j]);
+    }
+    // next round: `stride` rows on
+    __device__ __forceinline__ void begin(long long r, long long stride) {
+        stage = 0;
+#pragma unroll
+        for (int k = 0; k + 1 < kStages; ++k) fetch(r + k * stride, k);
+    }
+    __device__ __forceinline__ void ahead(long long r, long long stride) const {
+        fetch(r + (kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
+        wait();
+    }
+    __device__ __forceinline__ void step() { stage = stage + 1 == kStages ? 0 : stage + 1; }
+};
+
+template <typename T, int V, int NV, bool BIG, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_layernorm_rows(const T *x, const float *__restrict__ gamma,
+                                                         const float *__restrict__ beta, float eps, long long rows,
+                                                         int D, int tpr, T *z, float *mean, float *rstd) {
+    using L = Rows<T, V, NV, 1>;
+    constexpr int R = L::R;
+    __shared__ float buf[2 * R * 32];
+    extern __shared__ __align__(16) unsigned char ring[];
+    int turn = 0;
+    const int groups = blockDim.x / tpr, l = threadIdx.x % tpr;
+    const long long stride = (long long)gridDim.x * groups * R;
+    const float inv = 1.0f / (float)D;
+    const Weights<V, NV> ga(gamma, l, tpr, D), be(beta, l, tpr, D);
+    L in{reinterpret_cast<Pack<T, V> *>(ring), {x}, rows, D, l, tpr, 0};
+    // every group of a block takes the same number of turns (the barrier in group_sum)
+    const long long first = (long long)blockIdx.x * groups * R, mine = (threadIdx.x / tpr) * R;
+    in.begin(first + mine, stride);
+    for (long long r0 = first; r0 < rows; r0 += stride, in.step()) {
+        const long long r = r0 + mine;
+        in.ahead(r, stride);
+        float s[R], mu[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            s[q] = 0.0f;
+            if (r + q < rows)
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if ((l + i * tpr) * V < D) {
+                        float v[V];
+                        in.get(r, q, 0, i, v);
+#pragma unroll
+                        for (int j = 0; j < V; ++j) s[q] += v[j];
+                    }
+        }
+        group_sum<R, BIG>(s, tpr, buf, turn);
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            mu[q] = s[q] * inv;
+            s[q] = 0.0f;
+            if (r + q < rows)
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if ((l + i * tpr) * V < D) {
+                        float v[V];
+                        in.get(r, q, 0, i, v);
+#pragma unroll
+                        for (int j = 0; j < V; ++j) s[q] = fmaf(v[j] - mu[q], v[j] - mu[q], s[q]);
+                    }
+        }
+        group_sum<R, BIG>(s, tpr, buf, turn);
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            if (r + q >= rows) continue;
+            const float rs = 1.0f / sqrtf(fmaf(s[q], inv, eps));
+            if (l == 0) {
+                mean[r + q] = mu[q];
+                rstd[r + q] = rs;
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (l + i * tpr) * V;
+                if (c < D) {
+                    float o[V], g[V], b[V];
+                    ga.get(i, g);
+                    be.get(i, b);
+                    in.get(r, q, 0, i, o);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) o[j] = fmaf((o[j] - mu[q]) * rs, g[j], b[j]);
+                    store_pack<T, V>(z + (r + q) * D + c, o);
+                }
+            }
         }
     }
 }
 
 template <typename T, int V, int NV, bool BIG, int MAXT>
 __global__ void __launch_bounds__(MAXT) k_layernorm_rows_backward(
-    const T *__restrict__ dz, const T *__restrict__ x, const float *__restrict__ gamma,
-    const float *__restrict__ mean, const float *__restrict__ rstd, long long rows, int D, int tpr, T *dx,
-    float *part) {
-    __shared__ float buf[2 * 2 * 32];
-    extern __shared__ float sacc[];   // groups > 1: [2][D]
+    const T *dz, const T *x, const float *__restrict__ gamma, const float *__restrict__ mean,
+    const float *__restrict__ rstd, long long rows, int D, int tpr, T *dx, float *part) {
+    using L = Rows<T, V, NV, 2>;
+    constexpr int R = L::R;
+    __shared__ float buf[2 * 2 * R * 32];
+    extern __shared__ __align__(16) unsigned char ring[];   // groups > 1: at the end [2][D] floats in its place
     int turn = 0;
     const int groups = blockDim.x / tpr, l = threadIdx.x % tpr, gi = threadIdx.x / tpr;
     float dg[NV][V], db[NV][V];
@@ -115,47 +250,75 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_rows_backward(
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) dg[i][j] = db[i][j] = 0.0f;
+    const Weights<V, NV> ga(gamma, l, tpr, D);
     const float inv = 1.0f / (float)D;
-    const long long stride = (long long)gridDim.x * groups;
+    const long long stride = (long long)gridDim.x * groups * R;
+    L in{reinterpret_cast<Pack<T, V> *>(ring), {x, dz}, rows, D, l, tpr, 0};
+    float nm[R], nr[R];
+    auto stats = [&](long long r) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            nm[q] = r + q < rows ? __ldg(mean + r + q) : 0.0f;
+            nr[q] = r + q < rows ? __ldg(rstd + r + q) : 0.0f;
+        }
+    };
     // every group of a block takes the same number of turns (the barrier in group_sum)
-    for (long long r0 = (long long)blockIdx.x * groups; r0 < rows; r0 += stride) {
-        const long long row = r0 + gi;
-        const bool in = row < rows;
-        float xv[NV][V], h[NV][V];
-        float s[2] = {0.0f, 0.0f};
+    const long long first = (long long)blockIdx.x * groups * R, mine = gi * R;
+    in.begin(first + mine, stride);
+    stats(first + mine);
+    for (long long r0 = first; r0 < rows; r0 += stride, in.step()) {
+        const long long r = r0 + mine;
+        in.ahead(r, stride);
+        float s[2 * R], mu[R], rs[R];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (l + i * tpr) * V;
-            if (in && c < D) {
-                load_pack<T, V>(x + row * D + c, xv[i]);
-                load_pack<T, V>(dz + row * D + c, h[i]);
-            }
+        for (int q = 0; q < R; ++q) {
+            s[2 * q] = s[2 * q + 1] = 0.0f;
+            mu[q] = nm[q];
+            rs[q] = nr[q];
+            if (r + q < rows)
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if ((l + i * tpr) * V < D) {
+                        float v[V], d[V], g[V];
+                        ga.get(i, g);
+                        in.get(r, q, 0, i, v);
+                        in.get(r, q, 1, i, d);
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            const float xh = (v[j] - mu[q]) * rs[q], h = d[j] * g[j];
+                            dg[i][j] = fmaf(d[j], xh, dg[i][j]);
+                            db[i][j] += d[j];
+                            s[2 * q] += h;
+                            s[2 * q + 1] = fmaf(h, xh, s[2 * q + 1]);
+                        }
+                    }
         }
-        const float mu = in ? __ldg(mean + row) : 0.0f, rs = in ? __ldg(rstd + row) : 0.0f;
+        stats(r + stride);
+        group_sum<2 * R, BIG>(s, tpr, buf, turn);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (in && (l + i * tpr) * V < D)
+        for (int q = 0; q < R; ++q) {
+            if (r + q >= rows) continue;
+            const float m0 = s[2 * q] * inv, m1 = s[2 * q + 1] * inv;
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    xv[i][j] = (xv[i][j] - mu) * rs;
-                    dg[i][j] = fmaf(h[i][j], xv[i][j], dg[i][j]);
-                    db[i][j] += h[i][j];
-                    h[i][j] *= __ldg(gamma + (l + i * tpr) * V + j);
-                    s[0] += h[i][j];
-                    s[1] = fmaf(h[i][j], xv[i][j], s[1]);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (l + i * tpr) * V;
+                if (c < D) {
+                    float o[V], d[V], g[V];
+                    ga.get(i, g);
+                    in.get(r, q, 0, i, o);
+                    in.get(r, q, 1, i, d);
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        o[j] = rs[q] * (d[j] * g[j] - fmaf((o[j] - mu[q]) * rs[q], m1, m0));
+                    store_pack<T, V>(dx + (r + q) * D + c, o);
                 }
-        group_sum<2, BIG>(s, tpr, buf, turn);
-        const float m0 = s[0] * inv, m1 = s[1] * inv;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (l + i * tpr) * V;
-            if (in && c < D) {
-                float o[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = rs * (h[i][j] - fmaf(xv[i][j], m1, m0));
-                store_pack<T, V>(dx + row * D + c, o);
             }
         }
+    }
+    float *sacc = reinterpret_cast<float *>(ring);
+    if (groups > 1) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();   // the ring is used up
     }
     float *p = part + (size_t)blockIdx.x * 2 * D;
     if (groups > 1) {   // the block's groups one after the other
@@ -188,28 +351,23 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_rows_backward(
     }
 }
 
-// out0[c], out1[c] = sums over n partial rows [2][D]: 32 columns a block, 8
+// out0[c], out1[c] = sums over n partial rows [2][D]: 32 columns a block, 32
 // strided slices of the rows each, added in order
-__global__ void __launch_bounds__(256) k_sum_partials(const float *__restrict__ part, int n, int D, float *out0,
-                                                      float *out1) {
-    __shared__ float s[8][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+__global__ void __launch_bounds__(1024) k_sum_partials(const float *__restrict__ part, int n, int D, float *out0,
+                                                       float *out1) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, w = threadIdx.x >> 5;
     float a = 0.0f;
     if (c < 2 * D) {
-        int r = w;
-        for (; r + 24 < n; r += 32) {
-            const float v0 = part[(size_t)r * 2 * D + c], v1 = part[(size_t)(r + 8) * 2 * D + c];
-            const float v2 = part[(size_t)(r + 16) * 2 * D + c], v3 = part[(size_t)(r + 24) * 2 * D + c];
-            a += (v0 + v1) + (v2 + v3);
-        }
-        for (; r < n; r += 8) a += part[(size_t)r * 2 * D + c];
+#pragma unroll 8
+        for (int r = w; r < n; r += 32) a += part[(size_t)r * 2 * D + c];
     }
-    s[w][threadIdx.x & 31] = a;
+    s[w][lane] = a;
     __syncthreads();
     if (w == 0 && c < 2 * D) {
         float t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += s[i][threadIdx.x];
+        for (int i = 0; i < 32; ++i) t += s[i][lane];
         if (c < D)
             out0[c] = t;
         else
@@ -218,9 +376,9 @@ __global__ void __launch_bounds__(256) k_sum_partials(const float *__restrict__ 
 }
 
 // ---------------------------------------------------- channel layout ------
-// x, dz [Bt, H, L]: a tile is 64 time steps of one batch row, 16 threads x 4
+// x, dz [Bt, H, L]: a tile is some time steps of one batch row, W threads x 4
 // steps wide and 16 slices of the channels deep.
-constexpr int kSteps = 64, kSlices = 16;
+constexpr int kSlices = 16;
 
 __device__ __forceinline__ float4 add4(float4 a, float4 b) {
     return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
@@ -242,7 +400,8 @@ __device__ __forceinline__ float4 rstd4(float4 ss, float inv, float eps) {
 }
 
 // sum over the slices of a value per (slice, steps); two barriers
-__device__ __forceinline__ float4 slice_sum(float4 a, float4 (*red)[kSteps / 4], int hs, int tl) {
+template <int W>
+__device__ __forceinline__ float4 slice_sum(float4 a, float4 (*red)[W], int hs, int tl) {
     __syncthreads();
     red[hs][tl] = a;
     __syncthreads();
@@ -251,81 +410,137 @@ __device__ __forceinline__ float4 slice_sum(float4 a, float4 (*red)[kSteps / 4],
     for (int i = 1; i < kSlices; ++i) s = add4(s, red[i][tl]);
     return s;
 }
-// sum over the 16 threads of a slice
+// sum over the W threads of a slice
+template <int W>
 __device__ __forceinline__ float lane_sum(float v) {
 #pragma unroll
-    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = W / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// H <= 16 NV: x and dz of a tile stay in registers, and so do the weight
-// gradients of the thread's channels over all tiles of the block
+// Sums of N values per step over all channels, for 256 threads as 32 slices of
+// 8: within a warp by shuffles, then the eight warps' through shared memory, one
+// barrier, two buffers in turn.
+template <int N>
+__device__ __forceinline__ void step_sums(float4 (&a)[N], float4 (*red)[3][8][8], int &turn) {
+    const int lane = threadIdx.x & 31, tl = lane & 7, w = threadIdx.x >> 5;
+    float4 (*b)[8][8] = red[turn++ & 1];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1)
+            a[n] = add4(a[n], make_float4(__shfl_xor_sync(0xffffffffu, a[n].x, o), __shfl_xor_sync(0xffffffffu, a[n].y, o),
+                                          __shfl_xor_sync(0xffffffffu, a[n].z, o), __shfl_xor_sync(0xffffffffu, a[n].w, o)));
+        if (lane < 8) b[n][w][tl] = a[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        a[n] = b[n][0][tl];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) a[n] = add4(a[n], b[n][k][tl]);
+    }
+}
+
+// H <= 32 NV: tiles of 32 steps. Three tiles of x and dz are in shared memory
+// or on their way to it (a thread copies exactly what it reads, so a copy needs
+// no barrier), so that loads go on while a tile is reduced: with the loads of a
+// tile in registers behind each other's reductions the memory idled half the
+// time (8 x 256 x 16384: 109 us; now 82 us, 4.9 TB/s). The weight gradients of
+// a thread's channels stay in registers over all tiles of the block.
+constexpr int kChStages = 3;
+
 template <int NV>
 __global__ void __launch_bounds__(256) k_layernorm_channels_backward_reg(
     const float *__restrict__ dz, const float *__restrict__ x, const float *__restrict__ gamma, float eps, int Bt,
     int H, int L, float *dx, float *part) {
-    __shared__ float4 red[kSlices][kSteps / 4];
-    const int tl = threadIdx.x % (kSteps / 4), hs = threadIdx.x / (kSteps / 4);
+    __shared__ float4 red[2][3][8][8];
+    extern __shared__ __align__(16) float4 tiles_s[];   // [stages][x, dz][H][8]
+    constexpr int W = 8, kSteps = 4 * W;
+    const int tl = threadIdx.x % W, hs = threadIdx.x / W;
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float inv = 1.0f / (float)H;
-    float dg[NV], db[NV];
+    float dg[NV], db[NV], ga[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) dg[i] = db[i] = 0.0f;
-    const int tiles_l = (L + kSteps - 1) / kSteps;
+    for (int i = 0; i < NV; ++i) {
+        dg[i] = db[i] = 0.0f;
+        ga[i] = hs + 32 * i < H ? __ldg(gamma + hs + 32 * i) : 0.0f;
+    }
+    const unsigned tiles_l = (L + kSteps - 1) / kSteps;
     const long long tiles = (long long)tiles_l * Bt;
+    int turn = 0;
+    auto place = [&](long long tile, int &t) {   // the thread's first element of a tile, and its first step
+        const long long b = tile / tiles_l;
+        t = (int)(tile - b * tiles_l) * kSteps + 4 * tl;
+        return (size_t)b * H * L + t;
+    };
+    auto fetch = [&](long long tile, int st) {
+        int t;
+        if (tile < tiles) {
+            const size_t base = place(tile, t);
+            float4 *s = tiles_s + (size_t)st * 2 * H * W + tl;
+            if (t < L)   // L is a multiple of 16: t < L implies t + 3 < L
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int h = hs + 32 * i;
+                    if (h < H) {
+                        umma::cp_async16(s + h * W, x + base + (size_t)h * L);
+                        umma::cp_async16(s + (H + h) * W, dz + base + (size_t)h * L);
+                    }
+                }
+        }
+        umma::cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k + 1 < kChStages; ++k) fetch(blockIdx.x + (long long)k * gridDim.x, k);
+    int st = 0;
     for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int t = (int)(tile % tiles_l) * kSteps + 4 * tl;
-        const bool in = t < L;   // L is a multiple of 16: t < L implies t + 3 < L
-        const size_t base = (size_t)(tile / tiles_l) * H * L + t;
-        float4 v[NV], w[NV];
+        fetch(tile + (long long)(kChStages - 1) * gridDim.x, st == 0 ? kChStages - 1 : st - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kChStages - 1) : "memory");   // this tile's are the oldest
+        int t;
+        const size_t base = place(tile, t);
+        const bool in = t < L;
+        const float4 *sx = tiles_s + (size_t)st * 2 * H * W + tl;
+        st = st + 1 == kChStages ? 0 : st + 1;
+        float4 v[NV], w[NV], a[2] = {zero, zero}, s[2] = {zero, zero};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int h = hs + kSlices * i;
+            const int h = hs + 32 * i;
             const bool ok = in && h < H;
-            v[i] = ok ? *reinterpret_cast<const float4 *>(x + base + (size_t)h * L) : zero;
-            w[i] = ok ? *reinterpret_cast<const float4 *>(dz + base + (size_t)h * L) : zero;
+            v[i] = ok ? sx[h * W] : zero;
+            w[i] = ok ? sx[(H + h) * W] : zero;
+            a[0] = add4(a[0], v[i]);
+            a[1] = add4(a[1], scale4(w[i], ga[i]));
+            db[i] += sum4(w[i]);   // steps past L hold dz = 0
         }
-        float4 a = zero;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) a = add4(a, v[i]);
-        const float4 mu = scale4(slice_sum(a, red, hs, tl), inv);
-        a = zero;
+        step_sums<2>(a, red, turn);
+        const float4 mu = scale4(a[0], inv), m0 = scale4(a[1], inv);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (hs + kSlices * i < H) {
+            if (hs + 32 * i < H) {
                 v[i] = sub4(v[i], mu);
-                a = fma4(v[i], v[i], a);
+                s[0] = fma4(v[i], v[i], s[0]);
+                s[1] = fma4(scale4(w[i], ga[i]), v[i], s[1]);
             }
-        const float4 rs = rstd4(slice_sum(a, red, hs, tl), inv, eps);
-        float4 s0 = zero, s1 = zero;
+        step_sums<2>(s, red, turn);
+        const float4 rs = rstd4(s[0], inv, eps);
+        const float4 m1 = mul4(scale4(s[1], inv), mul4(rs, rs));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int h = hs + kSlices * i;
+            const int h = hs + 32 * i;
             if (h < H) {
-                v[i] = mul4(v[i], rs);
-                dg[i] += sum4(mul4(w[i], v[i]));   // steps past L hold dz = 0
-                db[i] += sum4(w[i]);
-                w[i] = scale4(w[i], __ldg(gamma + h));
-                s0 = add4(s0, w[i]);
-                s1 = fma4(w[i], v[i], s1);
+                dg[i] += sum4(mul4(w[i], mul4(v[i], rs)));
+                if (in)
+                    *reinterpret_cast<float4 *>(dx + base + (size_t)h * L) =
+                        mul4(rs, sub4(scale4(w[i], ga[i]), fma4(v[i], m1, m0)));
             }
         }
-        const float4 m0 = scale4(slice_sum(s0, red, hs, tl), inv);
-        const float4 m1 = scale4(slice_sum(s1, red, hs, tl), inv);
-        if (in)
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int h = hs + kSlices * i;
-                if (h < H)
-                    *reinterpret_cast<float4 *>(dx + base + (size_t)h * L) =
-                        mul4(rs, sub4(w[i], fma4(v[i], m1, m0)));
-            }
     }
     float *p = part + (size_t)blockIdx.x * 2 * H;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int h = hs + kSlices * i;
-        const float g = lane_sum(dg[i]), b = lane_sum(db[i]);
+        const int h = hs + 32 * i;
+        const float g = lane_sum<W>(dg[i]), b = lane_sum<W>(db[i]);
         if (h < H && tl == 0) {
             p[h] = g;
             p[H + h] = b;
@@ -339,9 +554,10 @@ __global__ void __launch_bounds__(256) k_layernorm_channels_backward_reg(
 __global__ void __launch_bounds__(256) k_layernorm_channels_backward(
     const float *__restrict__ dz, const float *__restrict__ x, const float *__restrict__ gamma, float eps, int Bt,
     int H, int L, float *dx, float *part) {
-    __shared__ float4 red[kSlices][kSteps / 4];
+    constexpr int W = 16, kSteps = 4 * W;
+    __shared__ float4 red[kSlices][W];
     extern __shared__ float sacc[];   // [2][H]
-    const int tl = threadIdx.x % (kSteps / 4), hs = threadIdx.x / (kSteps / 4);
+    const int tl = threadIdx.x % (W), hs = threadIdx.x / (W);
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float inv = 1.0f / (float)H;
     for (int c = threadIdx.x; c < 2 * H; c += 256) sacc[c] = 0.0f;
@@ -355,7 +571,7 @@ __global__ void __launch_bounds__(256) k_layernorm_channels_backward(
         if (in)
             for (int h = hs; h < H; h += kSlices)
                 a = add4(a, *reinterpret_cast<const float4 *>(x + base + (size_t)h * L));
-        const float4 mu = scale4(slice_sum(a, red, hs, tl), inv);
+        const float4 mu = scale4(slice_sum<W>(a, red, hs, tl), inv);
         float4 ss = zero, s0 = zero, s1 = zero;
         if (in)
             for (int h = hs; h < H; h += kSlices) {
@@ -365,9 +581,9 @@ __global__ void __launch_bounds__(256) k_layernorm_channels_backward(
                 s0 = add4(s0, w);
                 s1 = fma4(w, c, s1);
             }
-        const float4 rs = rstd4(slice_sum(ss, red, hs, tl), inv, eps);
-        const float4 m0 = scale4(slice_sum(s0, red, hs, tl), inv);
-        const float4 m1 = mul4(scale4(slice_sum(s1, red, hs, tl), inv), rs);
+        const float4 rs = rstd4(slice_sum<W>(ss, red, hs, tl), inv, eps);
+        const float4 m0 = scale4(slice_sum<W>(s0, red, hs, tl), inv);
+        const float4 m1 = mul4(scale4(slice_sum<W>(s1, red, hs, tl), inv), rs);
         const int hn = (H + kSlices - 1) / kSlices;
         for (int i = 0; i < hn; ++i) {   // the same count for all lanes: lane_sum is a warp operation
             const int h = hs + kSlices * i;
@@ -380,8 +596,8 @@ __global__ void __launch_bounds__(256) k_layernorm_channels_backward(
                 *reinterpret_cast<float4 *>(dx + base + (size_t)h * L) =
                     mul4(rs, sub4(scale4(d, __ldg(gamma + h)), fma4(xh, m1, m0)));
             }
-            g = lane_sum(g);
-            b = lane_sum(b);
+            g = lane_sum<W>(g);
+            b = lane_sum<W>(b);
             if (h < H && tl == 0) {
                 sacc[h] += g;
                 sacc[H + h] += b;
@@ -394,60 +610,79 @@ __global__ void __launch_bounds__(256) k_layernorm_channels_backward(
 }
 
 // How a row of D elements is spread: V per access, NV accesses by each of tpr
-// threads, at most 16 elements a thread (8 when single): registers hold the
-// row, its gradient and two weight gradients. D <= 8192 takes at most 512
-// threads, or 1024 with single elements.
+// threads, at most kForward or kBackward elements a thread (8 when single). As
+// few threads as that allows: a row's reductions and addresses cost every warp
+// of it the same. The backward pass keeps two sums an element, and at 32 of
+// them a thread too few warps fit (32768 rows of 1024 bf16: 97 us).
+constexpr int kForward = 32, kBackward = 16;
 struct RowPlan { int v, nv, tpr, block; };
 
-RowPlan row_plan(int D, int elem, bool vector) {
+RowPlan row_plan(int D, int elem, bool vector, int elements) {
     RowPlan p;
     p.v = vector ? 16 / elem : 1;
-    const int need = (D + p.v - 1) / p.v, most = vector ? 16 / p.v : 8;
+    const int need = (D + p.v - 1) / p.v, most = vector ? elements / p.v : 8;
     p.nv = 1;
     p.tpr = 1;
-    while (p.tpr < need && p.tpr < 256) p.tpr *= 2;
+    while (p.tpr < need && p.tpr < 32) p.tpr *= 2;
     while (p.tpr * p.nv < need && p.nv < most) p.nv *= 2;
-    while (p.tpr * p.nv < need) p.tpr *= 2;
-    p.block = p.tpr > 256 ? p.tpr : 256;
+    while (p.tpr * p.nv < need) p.tpr *= 2;   // D <= 8192: at most 512 threads, 1024 with single elements
+    // rows of more than a warp have a block each, whose barrier nobody else waits at
+    p.block = p.tpr > 32 ? p.tpr : 256;
     return p;
 }
 
-int backward_blocks(long long rows, const RowPlan &p) {
-    const long long need = (rows + p.block / p.tpr - 1) / (p.block / p.tpr);
-    return (int)(need < kBlocks ? need : kBlocks);
+// blocks for `rows` rows, at most `most`
+int row_blocks(long long rows, const RowPlan &p, int at_once, int most) {
+    const int per = p.block / p.tpr * at_once;
+    const long long need = (rows + per - 1) / per;
+    return (int)(need < most ? need : most);
 }
 
-// calls f with the plan's V, NV, whether a row spans warps, and the block size as constants
-template <typename T, typename F>
+// calls f with the plan's V, NV, whether a row spans warps, and the largest block as constants
+template <typename T, int ELEMENTS, typename F>
 void with_plan(const RowPlan &p, F &&f) {
+    using std::integral_constant;
     auto go = [&](auto v, auto most) {
         constexpr int V = decltype(v)::value, M = decltype(most)::value;
-        using std::integral_constant;
         integral_constant<int, 256> b256;
-        integral_constant<bool, true> big;
-        if (p.tpr <= 32)
-            f(v, integral_constant<int, 1>{}, integral_constant<bool, false>{}, b256);
-        else if (p.nv == 1)
-            f(v, integral_constant<int, 1>{}, big, b256);
-        else if (p.tpr > 512) {
-            if constexpr (V == 1) f(v, most, big, integral_constant<int, 1024>{});
-        } else if (p.tpr > 256)
-            f(v, most, big, integral_constant<int, 512>{});
-        else if (p.nv == M)
-            f(v, most, big, b256);
-        else if constexpr (M >= 4) {
-            if (p.nv == 2)
-                f(v, integral_constant<int, 2>{}, big, b256);
-            else
-                f(v, integral_constant<int, 4>{}, big, b256);
+        if (p.tpr > 256) {
+            f(v, most, integral_constant<bool, true>{}, integral_constant<int, V == 1 ? 1024 : 512>{});
+        } else if (p.tpr > 32) {
+            f(v, most, integral_constant<bool, true>{}, b256);
+        } else {
+            integral_constant<bool, false> small;
+            if (p.nv == 1)
+                f(v, integral_constant<int, 1>{}, small, b256);
+            else if (p.nv == 2)
+                f(v, integral_constant<int, 2>{}, small, b256);
+            else if constexpr (M >= 4) {
+                if (p.nv == 4) return f(v, integral_constant<int, 4>{}, small, b256);
+                if constexpr (M >= 8) f(v, integral_constant<int, 8>{}, small, b256);
+            }
         }
     };
     constexpr int VV = 16 / (int)sizeof(T);
     if (p.v == 1)
-        go(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
+        go(integral_constant<int, 1>{}, integral_constant<int, 8>{});
     else
-        go(std::integral_constant<int, VV>{}, std::integral_constant<int, 16 / VV>{});
+        go(integral_constant<int, VV>{}, integral_constant<int, ELEMENTS / VV>{});
 }
+
+// blocks of a kernel that an SM holds, asked for once per block size, which
+// sets the shared memory (the same on every device this library runs on)
+struct Resident {
+    int n[33] = {};   // by block size / 32
+    template <typename K>
+    int of(K *kernel, int block, size_t smem) {
+        int &r = n[block / 32];
+        if (r == 0) {
+            int b = 0;
+            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, block, smem) != cudaSuccess || b < 1) b = 1;
+            r = b;
+        }
+        return r;
+    }
+};
 
 template <typename F>
 void with_type(int dtype, F &&f) {
@@ -472,51 +707,79 @@ size_t norm_backward_workspace_bytes(int D) { return (size_t)kBlocks * 2 * D * s
 cudaError_t launch_layernorm_rows(int dtype, const void *x, const float *gamma, const float *beta, float eps,
                                   long long rows, int D, void *z, float *mean, float *rstd, cudaStream_t st) {
     if (rows == 0) return cudaSuccess;
-    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, vector_ok(dtype, D, x, z, nullptr));
-    const int groups = p.block / p.tpr;
-    const int grid = (int)((rows + groups - 1) / groups);
+    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, vector_ok(dtype, D, x, z, nullptr), kForward);
+    cudaError_t err = cudaSuccess;
     with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        with_plan<T>(p, [&](auto v, auto nv, auto big, auto most) {
-            k_layernorm_rows<T, decltype(v)::value, decltype(nv)::value, decltype(big)::value, decltype(most)::value>
-                <<<grid, p.block, 0, st>>>((const T *)x, gamma, beta, eps, rows, D, p.tpr, (T *)z, mean, rstd);
+        with_plan<T, kForward>(p, [&](auto v, auto nv, auto big, auto most) {
+            constexpr int V = decltype(v)::value, NV = decltype(nv)::value, MAXT = decltype(most)::value;
+            static Resident resident;
+            static SmemLimit limit;
+            auto *kernel = k_layernorm_rows<T, V, NV, decltype(big)::value, MAXT>;
+            const size_t smem = Rows<T, V, NV, 1>::bytes(p.block);
+            err = limit.raise(kernel, smem);
+            if (err != cudaSuccess) return;
+            const int grid = row_blocks(rows, p, rows_at_once<V, NV>(), 148 * resident.of(kernel, p.block, smem));
+            kernel<<<grid, p.block, smem, st>>>((const T *)x, gamma, beta, eps, rows, D, p.tpr, (T *)z, mean, rstd);
         });
     });
-    return cudaGetLastError();
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 cudaError_t launch_layernorm_rows_backward(int dtype, const void *dz, const void *x, const float *gamma,
                                            const float *mean, const float *rstd, long long rows, int D, void *dx,
                                            float *dgamma, float *dbeta, void *ws, cudaStream_t st) {
-    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, vector_ok(dtype, D, x, dz, dx));
-    const int grid = backward_blocks(rows, p);
-    // several groups in a block only for tpr <= 128 and one access each: D <= 1024
-    const size_t smem = p.block > p.tpr ? (size_t)2 * D * sizeof(float) : 0;
+    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, vector_ok(dtype, D, x, dz, dx), kBackward);
+    int grid = 0;
+    // several groups in a block only for tpr <= 32: D <= 1024
+    const size_t acc = p.block > p.tpr ? (size_t)2 * D * sizeof(float) : 0;
+    cudaError_t err = cudaSuccess;
     float *part = (float *)ws;
     if (rows > 0) with_type(dtype, [&](auto t) {   // no rows: zero gradients from no partial rows
         using T = decltype(t);
-        with_plan<T>(p, [&](auto v, auto nv, auto big, auto most) {
-            k_layernorm_rows_backward<T, decltype(v)::value, decltype(nv)::value, decltype(big)::value,
-                                      decltype(most)::value><<<grid, p.block, smem, st>>>(
+        with_plan<T, kBackward>(p, [&](auto v, auto nv, auto big, auto most) {
+            constexpr int V = decltype(v)::value, NV = decltype(nv)::value, MAXT = decltype(most)::value;
+            static SmemLimit limit;
+            auto *kernel = k_layernorm_rows_backward<T, V, NV, decltype(big)::value, MAXT>;
+            const size_t ring = Rows<T, V, NV, 2>::bytes(p.block), smem = ring > acc ? ring : acc;
+            err = limit.raise(kernel, smem);
+            if (err != cudaSuccess) return;
+            grid = row_blocks(rows, p, rows_at_once<V, NV>(), kBlocks);
+            kernel<<<grid, p.block, smem, st>>>(
                 (const T *)dz, (const T *)x, gamma, mean, rstd, rows, D, p.tpr, (T *)dx, part);
         });
     });
+    if (err != cudaSuccess) return err;
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    k_sum_partials<<<(2 * D + 31) / 32, 256, 0, st>>>(part, grid, D, dgamma, dbeta);
+    k_sum_partials<<<(2 * D + 31) / 32, 1024, 0, st>>>(part, grid, D, dgamma, dbeta);
     return cudaGetLastError();
 }
 
 cudaError_t launch_layernorm_channels_backward(const float *dz, const float *x, const float *gamma, float eps,
                                                int Bt, int H, int L, float *dx, float *dgamma, float *dbeta,
                                                void *ws, cudaStream_t st) {
-    const long long tiles = (long long)((L + kSteps - 1) / kSteps) * Bt;
-    const int grid = (int)(tiles < kBlocks ? tiles : kBlocks);
+    // tiles of 32 steps through shared memory up to 256 channels, of 64 steps read three times above
+    const bool staged = H <= 256;
+    const int steps = staged ? 32 : 64;
+    const long long tiles = (long long)((L + steps - 1) / steps) * Bt;
     float *part = (float *)ws;
-    if (H <= 4 * kSlices) {
-        k_layernorm_channels_backward_reg<4><<<grid, 256, 0, st>>>(dz, x, gamma, eps, Bt, H, L, dx, part);
-    } else if (H <= 16 * kSlices) {
-        k_layernorm_channels_backward_reg<16><<<grid, 256, 0, st>>>(dz, x, gamma, eps, Bt, H, L, dx, part);
+    int grid = (int)(tiles < kBlocks ? tiles : kBlocks);
+    if (staged) {
+        const int smem = kChStages * 2 * H * 128, most = 148 * (smem > 100 * 1024 ? 1 : smem > 50 * 1024 ? 2 : 4);
+        grid = (int)(tiles < most ? tiles : most);
+        auto go = [&](auto *f) {
+            if (smem > 40 * 1024) {
+                cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kChStages * 65536);
+                if (e != cudaSuccess) return e;
+            }
+            f<<<grid, 256, smem, st>>>(dz, x, gamma, eps, Bt, H, L, dx, part);
+            return cudaSuccess;
+        };
+        cudaError_t e = H <= 64 ? go(k_layernorm_channels_backward_reg<2>)
+                                : H <= 128 ? go(k_layernorm_channels_backward_reg<4>)
+                                           : go(k_layernorm_channels_backward_reg<8>);
+        if (e != cudaSuccess) return e;
     } else {
         const int smem = 2 * H * (int)sizeof(float);
         if (smem > 48 * 1024) {
@@ -529,7 +792,7 @@ cudaError_t launch_layernorm_channels_backward(const float *dz, const float *x, 
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    k_sum_partials<<<(2 * H + 31) / 32, 256, 0, st>>>(part, grid, H, dgamma, dbeta);
+    k_sum_partials<<<(2 * H + 31) / 32, 1024, 0, st>>>(part, grid, H, dgamma, dbeta);
     return cudaGetLastError();
 }
 

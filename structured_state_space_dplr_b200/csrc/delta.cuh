@@ -480,18 +480,16 @@ __device__ __forceinline__ void store16(T *o, long long row, const float (&x)[16
     }
 }
 
-// What the gradient kernel reads lies in groups of 8 consecutive elements of
-// one row, the rows of a group side by side: states as [dk / 8][dv][8] (a lane
-// of the chains, one v, stores 8 of its dk), E and dR as [dv / 8][64][8].
+// What the gradient kernel reads: states as [dk / 4][dv][4] (a lane of the
+// chains, one v, stores 4 of its dk; a warp 512 bytes in a row), E and dR as
+// [dv / 8][64][8], 8 consecutive elements of a row and the rows side by side.
 template <int HC>
 __device__ __forceinline__ void store_state(float *p, const float (&S)[HC], int h, int v, int dk, int dv) {
 #pragma unroll
-    for (int i = 0; i < HC; i += 8)
-        if (h * HC + i < dk) {
-            float4 *q = reinterpret_cast<float4 *>(p + ((size_t)((h * HC + i) / 8) * dv + v) * 8);
-            q[0] = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-            q[1] = make_float4(S[i + 4], S[i + 5], S[i + 6], S[i + 7]);
-        }
+    for (int i = 0; i < HC; i += 4)
+        if (h * HC + i < dk)
+            *reinterpret_cast<float4 *>(p + ((size_t)((h * HC + i) / 4) * dv + v) * 4) =
+                make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
 }
 __device__ __forceinline__ void store_tokens(float *p, const float (&x)[16], int j0, int v) {
     p += ((v >> 3) * kC + j0) * 8 + (v & 7);

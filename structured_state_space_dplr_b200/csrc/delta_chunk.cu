@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, const float *in
             const float4 *np = reinterpret_cast<const float4 *>(N + (size_t)d * a.dv + v0 + c0);
             const float4 p = __ldg(np), q = __ldg(np + 1);
             x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
-#pragma unroll 8
+#pragma unroll 32   // loads in flight: M comes from L2
             for (int c = 0; c < a.dk; ++c) {
                 const float m = __ldg(M + (size_t)c * a.dk + d);
                 const float4 u = *reinterpret_cast<const float4 *>(&S[c][c0]);

@@ -17,18 +17,21 @@
 // One block per chunk and key head, its value heads one after the other (their
 // dq and dk are summed in registers, in order). Tensor-memory lane = row of the
 // stacked [dR; dO], so dR's and dO's products share the instructions and the
-// scalings of rows are scalings of threads. Bound by memory: S0, dS1, E and dR
-// are 192 KB in float at Dk = Dv = 128, read once; they are split into bf16
-// parts here.
+// scalings of rows are scalings of threads. S0, dS1, E and dR are 192 KB in
+// float at Dk = Dv = 128, read once and split into bf16 parts here. (As parts,
+// stored by the chains and copied in bulk, they are half as much again, and
+// <S0, dS1> then costs the backward chain more than the copies save.)
 #include "delta.cuh"
 #include "s4dplr.h"
+
+#include <type_traits>
 
 namespace s4 {
 namespace {
 
 using namespace delta;
 
-constexpr int kGradThreads = 256;
+constexpr int kGradWarps = 8, kGradThreads = 32 * kGradWarps, kGradBlock = kGradThreads + 32;
 constexpr int kTrLd = kC + 1;
 
 // tensor-memory columns: the left operands' parts, X and F, [dR; dO] S0^T (later the sum of the last products), E dS1^T
@@ -72,13 +75,63 @@ __device__ __forceinline__ void column_sums(float (&w)[32], int lane) {
         }
 }
 
+__device__ __forceinline__ void zero8(float (&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+}
+
+// A state [dk / 4][dv][4] as right operand (rows v = K, columns dk), four pieces
+// of 8 on their way at a time; DOT: this thread's share of its dot with the
+// state whose parts lie there so far (their sums are its floats to 24 bits)
+template <int DKT, int DVT, bool DOT>
+__device__ __forceinline__ float put_state(unsigned char *dst, int part, const float *u, int dk, int dv, int tid) {
+    float both = 0.0f;
+#pragma unroll
+    for (int n0 = 0; n0 < DVT * DKT / 8; n0 += 4 * kGradThreads) {
+        float f[4][8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int n = n0 + k * kGradThreads + tid, v = n & (DVT - 1), dg = n / DVT;
+            zero8(f[k]);
+            if (n < DVT * DKT / 8 && v < dv && 8 * dg < dk) {
+                const float4 *q = reinterpret_cast<const float4 *>(u) + (size_t)2 * dg * dv + v;
+                const float4 x = __ldg(q), y = __ldg(q + dv);
+                f[k][0] = x.x, f[k][1] = x.y, f[k][2] = x.z, f[k][3] = x.w;
+                f[k][4] = y.x, f[k][5] = y.y, f[k][6] = y.z, f[k][7] = y.w;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int n = n0 + k * kGradThreads + tid, v = n & (DVT - 1), dg = n / DVT;
+            if (n < DVT * DKT / 8) {
+                unsigned char *to = dst + (v >> 3) * 128 + dg * (DVT * 16) + (v & 7) * 16;
+                if constexpr (DOT) {
+                    float z[8];
+                    zero8(z);
+#pragma unroll
+                    for (int q = 2; q >= 0; --q) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(to + q * part);
+                        const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) z[2 * j] += lo_f(r[j]), z[2 * j + 1] += hi_f(r[j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) both = fmaf(f[k][j], z[j], both);
+                }
+                put_parts(to, part, f[k]);
+            }
+        }
+    }
+    return both;
+}
+
 template <typename T>
 __device__ __forceinline__ void get8(const T *p, float (&f)[8]) {   // 16-bit types
     load_pack<T, 8>(p, f);
 }
 
 template <typename T, int DKT, int DVT>
-__global__ void __launch_bounds__(kGradThreads, 1)
+__global__ void __launch_bounds__(kGradBlock, 1)
     k_delta_gradient(DeltaArgs a, const T *dout, const unsigned char *images, const float *keep_s, const float *keep_e,
                      const float *keep_ds, const float *keep_dr, T *dq, T *dk, float *dg, float *dbeta,
                      unsigned *flags) {
@@ -144,27 +197,45 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         ok = umma::mbar_wait(bars + 2, turn2++ & 1, kSpinLimit) && ok;
         umma::fence_after_sync();
     };
-    // (+)= A [parts of K = 16 KS columns at kTmA] times an image's parts; n columns
-    auto times = [&](uint32_t d, uint32_t at, uint32_t lo, int ks_n, uint64_t b, uint32_t part, uint32_t step, uint32_t id,
-                     int nb, bool first) {
+    // D (+)= A [parts of K = 16 KS columns] times an image's PB parts
+    auto times = [&](auto ks_n, auto pb, uint32_t d, uint32_t at, uint32_t lo, uint64_t b, uint32_t part, uint32_t step,
+                     uint32_t id, bool first) {
 #pragma unroll
         for (int o = 2; o >= 0; --o)
 #pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                if (o - j < 0 || j >= nb) continue;
+            for (int j = 0; j < decltype(pb)::value; ++j) {
+                if (o - j < 0) continue;
                 const int p = o - j;
-                for (int ks = 0; ks < ks_n; ++ks) {
+#pragma unroll
+                for (int ks = 0; ks < decltype(ks_n)::value; ++ks) {
                     mma_ts(tm + d, tm + (p < 2 ? at + 16 * ks + 8 * p : lo + 8 * ks),
-                           b + ((uint64_t)(j * part + ks * step) >> 4), id, !first);
+                           b + ((j * part + ks * step) >> 4), id, !first);
                     first = false;
                 }
             }
     };
+    constexpr std::integral_constant<int, KV> kKv;
+    constexpr std::integral_constant<int, kC / 16> kKc;
+    constexpr std::integral_constant<int, 3> kThree;
+    constexpr std::integral_constant<int, NB> kNb;
+    // all that the heads of this block read on its way to L2
+    if (tid < 4 * per) {
+        const long long unit = slot * a.hv + hk * per + tid / 4;
+        const uint32_t st = (uint32_t)(a.dk * a.dv) * 4, tk = (uint32_t)(kC * a.dv) * 4;
+        switch (tid % 4) {
+            case 0: bulk_prefetch(keep_e + (size_t)unit * kC * a.dv, tk); break;
+            case 1: bulk_prefetch(keep_dr + (size_t)unit * kC * a.dv, tk); break;
+            case 2: bulk_prefetch(keep_s + (size_t)unit * a.dk * a.dv, st); break;
+            default: bulk_prefetch(keep_ds + (size_t)unit * a.dk * a.dv, st); break;
+        }
+    }
+    if (tid < rows)   // dO's rows too, the heads of this block side by side
+        for (int b = 0; b < per * a.dv * (int)sizeof(T); b += 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"((const char *)(dout + (tok + tid) * orow + (long long)hk * per * a.dv) + b));
 
-    // q_i.k_j and k_i.k_j, the same for all value heads
-    load_kq();
-    float raw[kC / 2];
-    if (warp == 0) {
+    if (warp == kGradWarps) {
+        // the products, by a warp of their own: issuing them takes as long as they take
+        load_kq();
         if (elect()) {
             bool acc = false;
 #pragma unroll
@@ -183,7 +254,46 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             umma::commit(bars + 1);
         }
         __syncwarp();
-    }
+        for (int g = 0; g < per; ++g) {
+            barrier();
+            barrier();
+            if (elect()) {
+                times(kKv, kThree, kTmXF, kTmA, kTmA + DVT, desc_k(e0, 1024, 128), L::kE, 2048, idesc(kC, false, false), true);
+                umma::commit(bars + 1);
+            }
+            __syncwarp();
+            barrier();
+            if (elect()) {
+                times(kKv, kThree, kTmD, kTmA, kTmA + DVT, desc_mn(s0, 128, DVT * 16), L::kS, 256, idesc(DKT, false, true),
+                      true);
+                umma::commit(bars + 2);
+            }
+            __syncwarp();
+            barrier();
+            if (elect()) {
+                times(kKv, kThree, kTmH, kTmA, kTmA + DVT, desc_mn(s0, 128, DVT * 16), L::kS, 256, idesc(DKT, false, true),
+                      true);
+                umma::commit(bars + 1);
+            }
+            __syncwarp();
+            if constexpr (!L::kBeside) {
+                barrier();
+                load_kq();
+            }
+            barrier();
+            if (elect()) {
+                times(kKc, kNb, kTmD, kTmA, kTmA + 64, desc_mn(kq0, 128, 2048), kPart, 256, idesc(DKT, false, true), true);
+                times(kKc, kNb, kTmD, kTmA + 96, kTmA + 160, desc_mn(kq0 + 1024, 128, 2048), kPart, 256,
+                      idesc(DKT, false, true), false);
+                umma::commit(bars + 2);
+            }
+            __syncwarp();
+            __syncthreads();
+        }
+    } else {
+    // q_i.k_j and k_i.k_j, the same for all value heads
+    load_kq();
+    float raw[kC / 2];
     wait1();
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
@@ -202,7 +312,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         const float *us = keep_s + (size_t)unit * a.dk * a.dv, *ud = keep_ds + (size_t)unit * a.dk * a.dv;
         const float *ue = keep_e + (size_t)unit * kC * a.dv, *ur = keep_dr + (size_t)unit * kC * a.dv;
         barrier();   // the last head's reads of shared and tensor memory
-        if (tid == 0) bulk_prefetch(ud, (uint32_t)(a.dk * a.dv) * 4);
         if (warp == 1) {
             const GateSums gt = gate_sums(a, tok, hv, rows, lane);
             const int j = 2 * lane;
@@ -217,53 +326,52 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             dec[j] = exp2f((float)(all - gt.x));
             dec[j + 1] = exp2f((float)(all - gt.y));
         }
-        // E as right operand: rows tokens, K = v
-        for (int n = tid; n < kC * DVT / 8; n += kGradThreads) {
-            const int t = n & (kC - 1), vg = n / kC;
-            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (8 * vg < a.dv) get8(ue + (size_t)n * 8, f);
-            put_parts(ei + (t >> 3) * 128 + vg * 1024 + (t & 7) * 16, L::kE, f);
-        }
-        // S0 as right operand: columns dk, K = v
-        for (int n = tid; n < DVT * DKT / 8; n += kGradThreads) {
-            const int v = n & (DVT - 1), dgr = n / DVT;
-            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (v < a.dv && 8 * dgr < a.dk) get8(us + ((size_t)dgr * a.dv + v) * 8, f);
-            put_parts(smem + (v >> 3) * 128 + dgr * (DVT * 16) + (v & 7) * 16, L::kS, f);
+        // E as right operand: rows tokens, K = v; four pieces of 8 on their way at a time
+#pragma unroll
+        for (int n0 = 0; n0 < kC * DVT / 8; n0 += 4 * kGradThreads) {
+            float f[4][8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int n = n0 + u * kGradThreads + tid;
+                zero8(f[u]);
+                if (n < kC * DVT / 8 && 8 * (n / kC) < a.dv) get8(ue + (size_t)n * 8, f[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int n = n0 + u * kGradThreads + tid, t = n & (kC - 1), vg = n / kC;
+                if (n < kC * DVT / 8) put_parts(ei + (t >> 3) * 128 + vg * 1024 + (t & 7) * 16, L::kE, f[u]);
+            }
         }
         // [dR; dO] as left operand, half of the columns a thread
 #pragma unroll
-        for (int n = 0; n < KV / 2; ++n) {
-            const int ks = half * (KV / 2) + n;
-            float x[16];
+        for (int n0 = 0; n0 < KV; n0 += 4) {
+            float f[4][8];
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int v = 16 * ks + 8 * m;
-                float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            for (int n = 0; n < 4; ++n) {
+                const int v = half * (DVT / 2) + 8 * (n0 + n);
+                zero8(f[n]);
                 if (v < a.dv) {
                     if (low)
-                        get8(ur + ((size_t)(v >> 3) * kC + i) * 8, f);
+                        get8(ur + ((size_t)(v >> 3) * kC + i) * 8, f[n]);
                     else if (i < rows)
-                        get8(dout + (tok + i) * orow + (long long)hv * a.dv + v, f);
+                        get8(dout + (tok + i) * orow + (long long)hv * a.dv + v, f[n]);
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[8 * m + j] = f[j];
             }
-            tm_split16(mine + kTmA + 16 * ks, mine + kTmA + DVT + 8 * ks, x);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int ks = half * (KV / 2) + n0 / 2 + n;
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = f[2 * n][j], x[8 + j] = f[2 * n + 1][j];
+                tm_split16(mine + kTmA + 16 * ks, mine + kTmA + DVT + 8 * ks, x);
+            }
         }
         barrier();
-        if (warp == 0) {
-            if (elect()) {
-                times(kTmXF, kTmA, kTmA + DVT, KV, desc_k(e0, 1024, 128), L::kE, 2048, idesc(kC, false, false), 3, true);
-                umma::commit(bars + 1);
-                times(kTmD, kTmA, kTmA + DVT, KV, desc_mn(s0, 128, DVT * 16), L::kS, 256, idesc(DKT, false, true), 3, true);
-                umma::commit(bars + 2);
-            }
-            __syncwarp();
-        }
+        // S0 as right operand, columns dk, K = v, beside the first product
+        put_state<DKT, DVT, false>(smem, L::kS, us, a.dk, a.dv, tid);
+        barrier();
         wait1();
-        float m[kC / 2];   // row i of N or M
-        {
+        {   // N and M, to shared memory for their columns
             const float2 Gi = Gs[i];
             const float mul = low ? 1.0f : a.scale;
             float cw[kC / 2], pw[kC / 2], rs = 0.0f;
@@ -281,8 +389,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                     cw[16 * n + t] = w * raw[16 * n + t];
                     pw[16 * n + t] = j <= i ? rs : 0.0f;   // what this half's columns before j hand to row i >= j
                     rs = fmaf(bs[j], cw[16 * n + t], rs);
-                    m[16 * n + t] = bs[j] * w;
-                    tr[((low ? 0 : kC) + i) * kTrLd + j] = m[16 * n + t];
+                    tr[R * kTrLd + j] = bs[j] * w;
                 }
             }
             if (half == 0) rsum[R] = rs;
@@ -306,59 +413,19 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 }
             }
         }
-        float both = 0.0f;   // <S0, dS1>
-        for (int n = tid; n < DVT * DKT / 8; n += kGradThreads) {
-            const int v = n & (DVT - 1), dgr = n / DVT;
-            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (v < a.dv && 8 * dgr < a.dk) {
-                float z[8];
-                get8(ud + ((size_t)dgr * a.dv + v) * 8, f);
-                get8(us + ((size_t)dgr * a.dv + v) * 8, z);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) both = fmaf(f[j], z[j], both);
-            }
-            put_parts(smem + (v >> 3) * 128 + dgr * (DVT * 16) + (v & 7) * 16, L::kS, f);
-        }
+        float both = put_state<DKT, DVT, true>(smem, L::kS, ud, a.dk, a.dv, tid);   // <S0, dS1>
 #pragma unroll
         for (int o = 16; o; o >>= 1) both += __shfl_xor_sync(0xffffffffu, both, o);
         if (lane == 0) red[warp] = both;
         barrier();
-        if (warp == 0) {
-            if (elect()) {
-                times(kTmH, kTmA, kTmA + DVT, KV, desc_mn(s0, 128, DVT * 16), L::kS, 256, idesc(DKT, false, true), 3, true);
-                umma::commit(bars + 1);
-            }
-            __syncwarp();
-        }
-        wait1();
-        if constexpr (!L::kBeside) {
-            barrier();
-            load_kq();
-        }
-        // left operands of the products with K (-(N + N^T); M) and Q (M^T; 0)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int j0 = half * (kC / 2) + 16 * n;
-            float x[16], y[16];
-#pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                const int j = j0 + t;
-                x[t] = low ? -(m[16 * n + t] + tr[j * kTrLd + i]) : m[16 * n + t];
-                y[t] = low ? tr[(kC + j) * kTrLd + i] : 0.0f;
-            }
-            tm_split16(mine + kTmA + j0, mine + kTmA + 64 + j0 / 2, x);
-            tm_split16(mine + kTmA + 96 + j0, mine + kTmA + 160 + j0 / 2, y);
-        }
-        // the products with the states: into dk or dq, and their dots with k or q
-        {
-            const float sr = low ? -eg[i] : a.scale * eg[i], hr = bs[i] * dec[i];
-            float d0 = 0.0f, d1 = 0.0f;
+        // a product with a state, into dk or dq and its dot with k or q
+        auto take = [&](uint32_t at, float scale) {
+            float d0 = 0.0f;
 #pragma unroll
             for (int n = 0; n < HK; n += 16) {
                 const int d = half * HK + n;
-                float x[16], y[16], k[16];
-                tm_ld16(mine + kTmD + d, x);
-                tm_ld16(mine + kTmH + d, y);
+                float x[16], k[16];
+                tm_ld16(mine + at + d, x);
                 const unsigned char *src = kq + (R >> 3) * 128 + (d >> 3) * 2048 + (R & 7) * 16;
 #pragma unroll
                 for (int t = 0; t < 16; ++t) k[t] = 0.0f;
@@ -377,26 +444,40 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
                 for (int t = 0; t < 16; ++t) {
                     d0 = fmaf(x[t], k[t], d0);
-                    acc[n + t] = fmaf(sr, x[t], acc[n + t]);
-                    if (low) {
-                        d1 = fmaf(y[t], k[t], d1);
-                        acc[n + t] = fmaf(hr, y[t], acc[n + t]);
-                    }
+                    acc[n + t] = fmaf(scale, x[t], acc[n + t]);
                 }
             }
-            dot[half * 2 * kC + R] = sr * d0;          // -e^G k.(S0 dR); scale e^G q.(S0 dO)
-            if (low) hdot[half * kC + i] = dec[i] * d1;
+            return d0;
+        };
+        // -e^G k.(S0 dR); scale e^G q.(S0 dO)
+        const float sr = low ? -eg[i] : a.scale * eg[i];
+        if constexpr (L::kBeside) dot[half * 2 * kC + R] = sr * take(kTmD, sr);   // beside the product
+        wait1();
+        if constexpr (!L::kBeside) {
+            barrier();
+            load_kq();
+            dot[half * 2 * kC + R] = sr * take(kTmD, sr);
+        }
+        // left operands of the products with K (-(N + N^T); M) and Q (M^T; 0)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int j0 = half * (kC / 2) + 16 * n;
+            float x[16], y[16];
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+                const int j = j0 + t;
+                x[t] = low ? -(tr[i * kTrLd + j] + tr[j * kTrLd + i]) : tr[R * kTrLd + j];
+                y[t] = low ? tr[(kC + j) * kTrLd + i] : 0.0f;
+            }
+            tm_split16(mine + kTmA + j0, mine + kTmA + 64 + j0 / 2, x);
+            tm_split16(mine + kTmA + 96 + j0, mine + kTmA + 160 + j0 / 2, y);
         }
         barrier();
-        if (warp == 0) {
-            if (elect()) {
-                times(kTmD, kTmA, kTmA + 64, kC / 16, desc_mn(kq0, 128, 2048), kPart, 256, idesc(DKT, false, true), NB, true);
-                times(kTmD, kTmA + 96, kTmA + 160, kC / 16, desc_mn(kq0 + 1024, 128, 2048), kPart, 256,
-                      idesc(DKT, false, true), NB, false);
-                umma::commit(bars + 2);
-            }
-            __syncwarp();
+        if (low) {   // H, beside the last products (warps 0, 1, 4 and 5)
+            const float d1 = take(kTmH, bs[i] * dec[i]);
+            hdot[half * kC + i] = dec[i] * d1;
         }
+        __syncthreads();
         if (warp == 1) {   // dbeta and dg, two tokens a lane
             float rect[2], u[2], r0[2], bh[2];
 #pragma unroll
@@ -412,7 +493,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
             float ss = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) ss += red[w];
+            for (int w = 0; w < kGradWarps; ++w) ss += red[w];
             // from this lane's first token on; before it
             float su = u[0] + u[1], sr = r0[0] + r0[1], sb = bh[0] + bh[1];
 #pragma unroll
@@ -456,6 +537,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 }
             }
     }
+    }
     if (!ok && flags && lane == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
     umma::fence_before_sync();
     __syncthreads();
@@ -472,7 +554,7 @@ cudaError_t run(const DeltaArgs &a, const void *dout, const void *ws, const floa
     cudaError_t e = limit.raise(k_delta_gradient<T, DKT, DVT>, smem);
     if (e != cudaSuccess) return e;
     const long long n = slots(a.tokens, a.n);
-    k_delta_gradient<T, DKT, DVT><<<(unsigned)(n * a.hk), kGradThreads, smem, st>>>(
+    k_delta_gradient<T, DKT, DVT><<<(unsigned)(n * a.hk), kGradBlock, smem, st>>>(
         a, (const T *)dout, (const unsigned char *)ws + (size_t)n * a.hv * kUnitBytes, keep_s, keep_e, keep_ds, keep_dr,
         (T *)dq, (T *)dk, dg, dbeta, flags);
     return cudaGetLastError();

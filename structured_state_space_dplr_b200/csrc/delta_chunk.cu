@@ -371,38 +371,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
 
 // The states before the segments: S <- M S + N from segment to segment. A block
 // has 16 columns of one sequence's and head's state in shared memory, a thread
-// one row of the result and 8 of the columns; M is read by columns from L2.
+// one row of the result and 8 of the columns; M [dk][dk] by columns comes into
+// shared memory one segment ahead (read from L2 in the loop a segment took
+// 11 us).
 constexpr int kJoinCols = 16;
-__global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, const float *init, const float *sums, float *starts) {
+__global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, const float *init, const float *sums, float *starts,
+                                                    unsigned *flags) {
+    extern __shared__ __align__(128) float Ms[];   // [2][dk][dk]
     __shared__ float S[128][kJoinCols];
+    __shared__ uint64_t full[2];
     const int hv = blockIdx.x % a.hv, s = blockIdx.x / a.hv, v0 = blockIdx.y * kJoinCols;
-    const int d = threadIdx.x & 127, c0 = (threadIdx.x >> 7) * 8;
+    const int d = threadIdx.x & 127, c0 = (threadIdx.x >> 7) * 8, mm = a.dk * a.dk;
     const int all = (sequence(a, s).len + kC - 1) / kC, n = (all + a.seg - 1) / a.seg;
     const long long first = segment0(a, s);
     const bool in = d < a.dk && v0 + c0 < a.dv;   // dv is a multiple of 8
+    auto summary = [&](int g) { return sums + (size_t)((first + g) * a.hv + hv) * a.dk * (a.dv + a.dk); };
+    auto fetch = [&](int g) {   // by one thread
+        umma::fence_proxy_async();
+        mbar_expect(full + (g & 1), mm * 4);
+        bulk_load(Ms + (g & 1) * mm, summary(g) + (size_t)a.dk * a.dv, mm * 4, full + (g & 1));
+        mbar_arrive(full + (g & 1));
+    };
+    if (threadIdx.x == 0) {
+        umma::mbar_init(full, 1);
+        umma::mbar_init(full + 1, 1);
+        umma::fence_mbar_init();
+        if (n > 1) fetch(0);
+    }
     float x[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         x[j] = in && init ? __ldg(init + (((size_t)s * a.hv + hv) * a.dk + d) * a.dv + v0 + c0 + j) : 0.0f;
+    bool ok = true;
     for (int g = 0;; ++g) {
-        const size_t unit = (size_t)(first + g) * a.hv + hv;
         if (in) {
-            float4 *to = reinterpret_cast<float4 *>(starts + (unit * a.dk + d) * a.dv + v0 + c0);
+            float4 *to = reinterpret_cast<float4 *>(starts + ((size_t)((first + g) * a.hv + hv) * a.dk + d) * a.dv + v0 + c0);
             to[0] = make_float4(x[0], x[1], x[2], x[3]);
             to[1] = make_float4(x[4], x[5], x[6], x[7]);
         }
         if (g + 1 >= n) break;
+        float4 p, q;
+        if (in) {
+            const float4 *np = reinterpret_cast<const float4 *>(summary(g) + (size_t)d * a.dv + v0 + c0);
+            p = __ldg(np);
+            q = __ldg(np + 1);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) S[d][c0 + j] = x[j];
-        __syncthreads();
-        const float *N = sums + unit * a.dk * (a.dv + a.dk), *M = N + (size_t)a.dk * a.dv;
+        __syncthreads();   // S is there; the other half of Ms is used up
+        if (threadIdx.x == 0 && g + 2 < n) fetch(g + 1);
+        ok = umma::mbar_wait(full + (g & 1), (g >> 1) & 1, kSpinLimit) && ok;
         if (in) {
-            const float4 *np = reinterpret_cast<const float4 *>(N + (size_t)d * a.dv + v0 + c0);
-            const float4 p = __ldg(np), q = __ldg(np + 1);
             x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
-#pragma unroll 32   // loads in flight: M comes from L2
+            const float *M = Ms + (g & 1) * mm + d;
+#pragma unroll 8
             for (int c = 0; c < a.dk; ++c) {
-                const float m = __ldg(M + (size_t)c * a.dk + d);
+                const float m = M[c * a.dk];
                 const float4 u = *reinterpret_cast<const float4 *>(&S[c][c0]);
                 const float4 w = *reinterpret_cast<const float4 *>(&S[c][c0 + 4]);
                 x[0] = fmaf(m, u.x, x[0]);
@@ -417,6 +441,7 @@ __global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, const float *in
         }
         __syncthreads();
     }
+    if (!ok && flags && threadIdx.x == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
 }
 
 template <typename T, int DKT>
@@ -434,7 +459,11 @@ cudaError_t run(const DeltaArgs &a, const float *init, float *last, const void *
         if (e != cudaSuccess) return e;
         k_delta_forward<T, DKT, true><<<(unsigned)(2 * blocks), kThreads, smem, st>>>(a, init, nullptr, sums, nullptr, units,
                                                                                     images, nullptr, nullptr, flags);
-        k_delta_join<<<dim3(a.n * a.hv, (a.dv + kJoinCols - 1) / kJoinCols), 256, 0, st>>>(a, init, sums, starts);
+        static SmemLimit limit_join;
+        e = limit_join.raise(k_delta_join, 2 * 128 * 128 * sizeof(float));
+        if (e != cudaSuccess) return e;
+        k_delta_join<<<dim3(a.n * a.hv, (a.dv + kJoinCols - 1) / kJoinCols), 256, 2 * a.dk * a.dk * sizeof(float), st>>>(
+            a, init, sums, starts, flags);
     }
     k_delta_forward<T, DKT, false><<<(unsigned)blocks, kThreads, smem, st>>>(a, init, last, nullptr, starts, units, images,
                                                                             keep_s, keep_e, flags);
@@ -446,9 +475,9 @@ cudaError_t run(const DeltaArgs &a, const float *init, float *last, const void *
 // Few long chains leave most SMs idle: then every sequence is cut into segments,
 // what each does to the state is computed for all at once (twice the chain's
 // work: M and N), joined, and the segments run again from their states. Times
-// in chunks of a chain (2.9 us; M and N without output 0.85 of that, a join
-// 1.5, the extra launches 4), for sequences of average length. One sequence of
-// 65536 tokens, 8 heads of 128: 3515 us in one piece.
+// in chunks of a chain (3.1 us; M and N without output 0.85 of that, a join
+// 0.8, the extra launches 4), for sequences of average length. One sequence of
+// 65536 tokens, 8 heads of 128: 3515 us in one piece, SEGMENTED in 18.
 int delta_segment(long long tokens, int n, int hv) {
     constexpr double kSms = 148;
     const double chains = (double)n * hv, c = ceil((double)tokens / kC / n);
@@ -456,7 +485,7 @@ int delta_segment(long long tokens, int n, int hv) {
     int seg = 0;
     for (int k = 3; k <= 64 && k <= c; ++k) {
         const double len = ceil(c / k), t = ceil(2 * chains * (k - 1) / kSms) * len * 0.85 +
-                                            ceil(chains * k / kSms) * len + 1.5 * k + 4;
+                                            ceil(chains * k / kSms) * len + 0.8 * k + 4;
         if (t < best) {
             best = t;
             seg = (int)len;

@@ -35,32 +35,43 @@ struct PrepSmem {
     static constexpr int kImg = kq_bytes<T, DKT>() > kMat ? kq_bytes<T, DKT>() : kMat;
     static constexpr int kParts = kMat + 3 * kTImg;
     static constexpr int kBig = kImg + kMat > kParts ? kImg + kMat : kParts;
-    static constexpr int kBytes = kBig + 4 * kC * 4 + 64;
+    static constexpr int kBytes = kBig + 6 * kC * 4 + 64;
 };
 
-// D[m x n] (rows r0, columns c0 of Y) = sign * X[m x k] Z[k x n] for float matrices of row stride kLd; 4 columns of one
-// row a thread and pass
-template <int M, int N, int K, bool NEG, typename FY>
-__device__ __forceinline__ void small_product(const float *X, const float *Z, int t, int nt, FY &&put) {
-    for (int i = t; i < M * N / 4; i += nt) {
-        const int r = i / (N / 4), c = i % (N / 4) * 4;
-        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+// put(row, column, 4 values) for +-X Z, N x N float matrices of row stride kLd, by
+// the first N * N / 8 of the threads, 2 x 4 values each (of 1, 2 and 4 rows a
+// thread the least time: more rows load less, but fewer warps wait longer)
+template <int N, bool NEG, typename F>
+__device__ __forceinline__ void small_product(const float *X, const float *Z, int t, F &&put) {
+    if (t >= N * N / 8) return;
+    const int r0 = t / (N / 4) * 2, c = t % (N / 4) * 4;
+    float y[2][4];
 #pragma unroll
-        for (int k = 0; k < K; k += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(X + r * kLd + k);
-            const float xs[4] = {x.x, x.y, x.z, x.w};
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 z = *reinterpret_cast<const float4 *>(Z + (k + j) * kLd + c);
-                const float v = NEG ? -xs[j] : xs[j];
-                y.x = fmaf(v, z.x, y.x);
-                y.y = fmaf(v, z.y, y.y);
-                y.z = fmaf(v, z.z, y.z);
-                y.w = fmaf(v, z.w, y.w);
-            }
+        for (int j = 0; j < 4; ++j) y[i][j] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+        float x[2][4], z[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 w = *reinterpret_cast<const float4 *>(Z + (k + i) * kLd + c);
+            z[i][0] = w.x, z[i][1] = w.y, z[i][2] = w.z, z[i][3] = w.w;
         }
-        put(r, c, y);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 u = *reinterpret_cast<const float4 *>(X + (r0 + i) * kLd + k);
+            x[i][0] = u.x, x[i][1] = u.y, x[i][2] = u.z, x[i][3] = u.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[i][j] = fmaf(NEG ? -x[i][q] : x[i][q], z[q][j], y[i][j]);
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) put(r0 + i, c, make_float4(y[i][0], y[i][1], y[i][2], y[i][3]));
 }
 
 template <typename T, int DKT>
@@ -73,8 +84,8 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
     unsigned char *parts = smem + kMat;
     // G / ln 2 as a float and what it leaves out: differences of large sums keep float's accuracy
     float2 *Gs = reinterpret_cast<float2 *>(smem + L::kBig);
-    float *cs = reinterpret_cast<float *>(Gs + kC), *bs = cs + kC;
-    uint64_t *bar = reinterpret_cast<uint64_t *>(bs + kC);
+    float *cs = reinterpret_cast<float *>(Gs + kC), *bs = cs + kC, *ds = bs + kC, *rs = ds + kC;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(rs + kC);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 1);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
@@ -107,6 +118,13 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
         const double end = __shfl_sync(0xffffffffu, y, lane | 7), all = __shfl_sync(0xffffffffu, y, 31);
         cs[j] = b0 * exp2f((float)(end - x));
         cs[j + 1] = b1 * exp2f((float)(end - y));
+        // within the 16 tokens: from G of their first, while both factors are far from float's limits (2^60)
+        const double first = __shfl_sync(0xffffffffu, x, lane & 24);
+        const bool near = first - end < 60.0;
+        rs[j] = near ? exp2f((float)(x - first)) : -1.0f;
+        rs[j + 1] = near ? exp2f((float)(y - first)) : -1.0f;
+        ds[j] = b0 * exp2f((float)(near ? first - x : 0.0));
+        ds[j + 1] = b1 * exp2f((float)(near ? first - y : 0.0));
         float *fac = reinterpret_cast<float *>(ws + (size_t)blockIdx.x * kUnitBytes + kTpBytes);
         *reinterpret_cast<float2 *>(fac + j) = make_float2(exp2f(xf), exp2f(yf));
         *reinterpret_cast<float2 *>(fac + kC + j) =
@@ -162,6 +180,19 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
         for (int n = 0; n < 2; ++n) {
             const int c = 32 * half + 16 * n;
             float d[16];
+            if (c / 16 > (i | 31) >> 4) {   // above the diagonal for the whole warp
+                if (is_p) {
+                    const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    tm_st8(mine + c, z);
+                    tm_st8(mine + c + 8, z);
+                    tm_st8(mine + 64 + c / 2, z);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<float4 *>(As + i * kLd + c + j) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+                continue;
+            }
             tm_ld16(mine + c, d);
             if (c / 16 < ib) {   // all columns are earlier tokens: one factor for the row, one for each column
                 const float rf = mul * decay(c + 15);
@@ -171,8 +202,16 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
                 for (int j = 0; j < 16; ++j) d[j] *= rf * e[j];
             } else if (c / 16 == ib) {
                 const int m = is_p ? i + 1 : i;
+                const float rf = rs[i];
+                if (rf >= 0.0f) {   // the same for the 16 tokens
+                    float e[16];
+                    get16(ds + c, e);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) d[j] = c + j < m ? d[j] * (mul * bs[c + j]) * decay(c + j) : 0.0f;
+                    for (int j = 0; j < 16; ++j) d[j] = c + j < m ? d[j] * (mul * rf * e[j]) : 0.0f;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) d[j] = c + j < m ? d[j] * (mul * bs[c + j]) * decay(c + j) : 0.0f;
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) d[j] = 0.0f;
@@ -214,11 +253,11 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
     // the 32 x 32 ones; A21 T11 goes where A12 = 0 lies
     {
         const int o = 32 * half, t = tid & 127;
-        small_product<16, 16, 16, false>(As + (o + 16) * kLd + o, Ts + o * kLd + o, t, 128, [&](int r, int c, float4 y) {
+        small_product<16, false>(As + (o + 16) * kLd + o, Ts + o * kLd + o, t, [&](int r, int c, float4 y) {
             *reinterpret_cast<float4 *>(As + (o + r) * kLd + o + 16 + c) = y;
         });
         __syncthreads();
-        small_product<16, 16, 16, true>(Ts + (o + 16) * kLd + o + 16, As + o * kLd + o + 16, t, 128,
+        small_product<16, true>(Ts + (o + 16) * kLd + o + 16, As + o * kLd + o + 16, t,
                                         [&](int r, int c, float4 y) {
                                             *reinterpret_cast<float4 *>(Ts + (o + 16 + r) * kLd + o + c) = y;
                                             *reinterpret_cast<float4 *>(Ts + (o + r) * kLd + o + 16 + c) =
@@ -226,11 +265,11 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
                                         });
     }
     __syncthreads();
-    small_product<32, 32, 32, false>(As + 32 * kLd, Ts, tid, 256, [&](int r, int c, float4 y) {
+    small_product<32, false>(As + 32 * kLd, Ts, tid, [&](int r, int c, float4 y) {
         *reinterpret_cast<float4 *>(As + r * kLd + 32 + c) = y;
     });
     __syncthreads();
-    small_product<32, 32, 32, true>(Ts + 32 * kLd + 32, As + 32, tid, 256, [&](int r, int c, float4 y) {
+    small_product<32, true>(Ts + 32 * kLd + 32, As + 32, tid, [&](int r, int c, float4 y) {
         *reinterpret_cast<float4 *>(Ts + (32 + r) * kLd + c) = y;
     });
     __syncthreads();
@@ -243,6 +282,13 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
             uint32_t w[4][3];
             const bool in = cg <= r / 8;   // the lower triangle; columns behind the diagonal's block are not read above it
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
+            if (8 * cg > (r | 31)) {   // above the diagonal for the whole warp
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+                    *reinterpret_cast<uint4 *>(parts + q * kTImg + (r >> 3) * 128 + cg * 1024 + (r & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                continue;
+            }
             if (in) {
                 x = *reinterpret_cast<const float4 *>(Ts + r * kLd + 8 * cg);
                 y = *reinterpret_cast<const float4 *>(Ts + r * kLd + 8 * cg + 4);

@@ -40,7 +40,7 @@ constexpr int kTmA = 0, kTmXF = 192, kTmD = 256, kTmH = 384;
 template <typename T, int DKT, int DVT>
 struct GradSmem {
     static constexpr int kS = DVT * DKT * 2, kE = kC * DVT * 2, kKq = kq_bytes<T, DKT>();   // one part of S0 or dS1, of E; all of [K; Q]
-    static constexpr int kSmall = 2 * kC * kTrLd * 4 + kC * 8 + 19 * kC * 4 + 128;
+    static constexpr int kSmall = 2 * kC * kTrLd * 4 + kC * 8 + 22 * kC * 4 + 128;
     // [K; Q] stays beside the states' image where there is room for both
     static constexpr bool kBeside = 3 * kS + 3 * kE + kKq + kSmall <= 232448;
     static constexpr int kArea = kBeside ? 3 * kS + kKq : (3 * kS > kKq ? 3 * kS : kKq);
@@ -80,47 +80,46 @@ __device__ __forceinline__ void zero8(float (&f)[8]) {
     for (int j = 0; j < 8; ++j) f[j] = 0.0f;
 }
 
-// A state [dk / 4][dv][4] as right operand (rows v = K, columns dk), four pieces
-// of 8 on their way at a time; DOT: this thread's share of its dot with the
-// state whose parts lie there so far (their sums are its floats to 24 bits)
+// A state [dk / 4][dv][4] as right operand (rows v = K, columns dk): four pieces
+// of 8 a thread at a time, the n0-th ones; first from memory, then as parts into
+// the image. DOT: this thread's share of the dot with the state whose parts lie
+// there so far (their sums are its floats to 24 bits).
+template <int DKT, int DVT>
+__device__ __forceinline__ void get_state(float (&f)[4][8], int n0, const float *u, int dk, int dv, int tid) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int n = (4 * n0 + k) * kGradThreads + tid, v = n & (DVT - 1), dg = n / DVT;
+        zero8(f[k]);
+        if (n < DVT * DKT / 8 && v < dv && 8 * dg < dk) {
+            const float4 *q = reinterpret_cast<const float4 *>(u) + (size_t)2 * dg * dv + v;
+            const float4 x = __ldg(q), y = __ldg(q + dv);
+            f[k][0] = x.x, f[k][1] = x.y, f[k][2] = x.z, f[k][3] = x.w;
+            f[k][4] = y.x, f[k][5] = y.y, f[k][6] = y.z, f[k][7] = y.w;
+        }
+    }
+}
 template <int DKT, int DVT, bool DOT>
-__device__ __forceinline__ float put_state(unsigned char *dst, int part, const float *u, int dk, int dv, int tid) {
+__device__ __forceinline__ float put_state(unsigned char *dst, int part, const float (&f)[4][8], int n0, int tid) {
     float both = 0.0f;
 #pragma unroll
-    for (int n0 = 0; n0 < DVT * DKT / 8; n0 += 4 * kGradThreads) {
-        float f[4][8];
+    for (int k = 0; k < 4; ++k) {
+        const int n = (4 * n0 + k) * kGradThreads + tid, v = n & (DVT - 1), dg = n / DVT;
+        if (n >= DVT * DKT / 8) break;
+        unsigned char *to = dst + (v >> 3) * 128 + dg * (DVT * 16) + (v & 7) * 16;
+        if constexpr (DOT) {
+            float z[8];
+            zero8(z);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int n = n0 + k * kGradThreads + tid, v = n & (DVT - 1), dg = n / DVT;
-            zero8(f[k]);
-            if (n < DVT * DKT / 8 && v < dv && 8 * dg < dk) {
-                const float4 *q = reinterpret_cast<const float4 *>(u) + (size_t)2 * dg * dv + v;
-                const float4 x = __ldg(q), y = __ldg(q + dv);
-                f[k][0] = x.x, f[k][1] = x.y, f[k][2] = x.z, f[k][3] = x.w;
-                f[k][4] = y.x, f[k][5] = y.y, f[k][6] = y.z, f[k][7] = y.w;
+            for (int q = 2; q >= 0; --q) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(to + q * part);
+                const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[2 * j] += lo_f(r[j]), z[2 * j + 1] += hi_f(r[j]);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) both = fmaf(f[k][j], z[j], both);
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int n = n0 + k * kGradThreads + tid, v = n & (DVT - 1), dg = n / DVT;
-            if (n < DVT * DKT / 8) {
-                unsigned char *to = dst + (v >> 3) * 128 + dg * (DVT * 16) + (v & 7) * 16;
-                if constexpr (DOT) {
-                    float z[8];
-                    zero8(z);
-#pragma unroll
-                    for (int q = 2; q >= 0; --q) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(to + q * part);
-                        const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) z[2 * j] += lo_f(r[j]), z[2 * j + 1] += hi_f(r[j]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) both = fmaf(f[k][j], z[j], both);
-                }
-                put_parts(to, part, f[k]);
-            }
-        }
+        put_parts(to, part, f[k]);
     }
     return both;
 }
@@ -143,7 +142,8 @@ __global__ void __launch_bounds__(kGradBlock, 1)
     float2 *Gs = reinterpret_cast<float2 *>(tr + 2 * kC * kTrLd);
     float *bs = reinterpret_cast<float *>(Gs + kC);                          // beta
     float *eg = bs + kC, *dec = eg + kC;                                     // e^G, e^(G_C - G)
-    float *csum = dec + kC;                                                  // [4][64]
+    float *ce = dec + kC, *de = ce + kC, *rf = de + kC;                      // factors of e^(G_i - G_j)
+    float *csum = rf + kC;                                                   // [4][64]
     float *gsum = csum + 4 * kC, *rsum = gsum + 4 * kC;                      // [4][64], [128]
     float *dot = rsum + 2 * kC, *hdot = dot + 4 * kC;                        // [2][128], [2][64]
     float *red = hdot + 2 * kC;                                              // [8]
@@ -218,7 +218,8 @@ __global__ void __launch_bounds__(kGradBlock, 1)
     constexpr std::integral_constant<int, kC / 16> kKc;
     constexpr std::integral_constant<int, 3> kThree;
     constexpr std::integral_constant<int, NB> kNb;
-    // all that the heads of this block read on its way to L2
+    // all that the heads of this block read on its way to L2 (for the block that
+    // follows on the SM as well, it would not all stay there: 1228 us for 1075)
     if (tid < 4 * per) {
         const long long unit = slot * a.hv + hk * per + tid / 4;
         const uint32_t st = (uint32_t)(a.dk * a.dv) * 4, tk = (uint32_t)(kC * a.dv) * 4;
@@ -325,27 +326,20 @@ __global__ void __launch_bounds__(kGradBlock, 1)
             eg[j + 1] = exp2f(yf);
             dec[j] = exp2f((float)(all - gt.x));
             dec[j + 1] = exp2f((float)(all - gt.y));
+            // e^(G_i - G_j) as two factors: by G at the end of j's 16 tokens where i is behind them; within
+            // the 16 by G of their first, while both factors are far from float's limits (2^60)
+            const double end = __shfl_sync(0xffffffffu, gt.y, lane | 7), first = __shfl_sync(0xffffffffu, gt.x, lane & 24);
+            const bool near = first - end < 60.0;
+            ce[j] = exp2f((float)(end - gt.x));
+            ce[j + 1] = exp2f((float)(end - gt.y));
+            rf[j] = near ? exp2f((float)(gt.x - first)) : -1.0f;
+            rf[j + 1] = near ? exp2f((float)(gt.y - first)) : -1.0f;
+            de[j] = exp2f((float)(near ? first - gt.x : 0.0));
+            de[j + 1] = exp2f((float)(near ? first - gt.y : 0.0));
         }
-        // E as right operand: rows tokens, K = v; four pieces of 8 on their way at a time
-#pragma unroll
-        for (int n0 = 0; n0 < kC * DVT / 8; n0 += 4 * kGradThreads) {
-            float f[4][8];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int n = n0 + u * kGradThreads + tid;
-                zero8(f[u]);
-                if (n < kC * DVT / 8 && 8 * (n / kC) < a.dv) get8(ue + (size_t)n * 8, f[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int n = n0 + u * kGradThreads + tid, t = n & (kC - 1), vg = n / kC;
-                if (n < kC * DVT / 8) put_parts(ei + (t >> 3) * 128 + vg * 1024 + (t & 7) * 16, L::kE, f[u]);
-            }
-        }
-        // [dR; dO] as left operand, half of the columns a thread
-#pragma unroll
-        for (int n0 = 0; n0 < KV; n0 += 4) {
-            float f[4][8];
+        // E as right operand (rows tokens, K = v) and [dR; dO] as left operand
+        // (half of the columns a thread); one's loads beside the other's parts
+        auto get_x = [&](float (&f)[4][8], int n0) {
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const int v = half * (DVT / 2) + 8 * (n0 + n);
@@ -357,6 +351,8 @@ __global__ void __launch_bounds__(kGradBlock, 1)
                         get8(dout + (tok + i) * orow + (long long)hv * a.dv + v, f[n]);
                 }
             }
+        };
+        auto put_x = [&](const float (&f)[4][8], int n0) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int ks = half * (KV / 2) + n0 / 2 + n;
@@ -365,10 +361,34 @@ __global__ void __launch_bounds__(kGradBlock, 1)
                 for (int j = 0; j < 8; ++j) x[j] = f[2 * n][j], x[8 + j] = f[2 * n + 1][j];
                 tm_split16(mine + kTmA + 16 * ks, mine + kTmA + DVT + 8 * ks, x);
             }
+        };
+        float f[4][8];
+        {
+            float fx[4][8];
+            get_x(fx, 0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int n = u * kGradThreads + tid;
+                zero8(f[u]);
+                if (n < kC * DVT / 8 && 8 * (n / kC) < a.dv) get8(ue + (size_t)n * 8, f[u]);
+            }
+            put_x(fx, 0);
+            if constexpr (KV > 4) get_x(fx, 4);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int n = u * kGradThreads + tid, t = n & (kC - 1), vg = n / kC;
+                if (n < kC * DVT / 8) put_parts(ei + (t >> 3) * 128 + vg * 1024 + (t & 7) * 16, L::kE, f[u]);
+            }
+            get_state<DKT, DVT>(f, 0, us, a.dk, a.dv, tid);
+            if constexpr (KV > 4) put_x(fx, 4);
         }
         barrier();
         // S0 as right operand, columns dk, K = v, beside the first product
-        put_state<DKT, DVT, false>(smem, L::kS, us, a.dk, a.dv, tid);
+        put_state<DKT, DVT, false>(smem, L::kS, f, 0, tid);
+        if constexpr (DVT * DKT / 8 > 4 * kGradThreads) {
+            get_state<DKT, DVT>(f, 1, us, a.dk, a.dv, tid);
+            put_state<DKT, DVT, false>(smem, L::kS, f, 1, tid);
+        }
         barrier();
         wait1();
         {   // N and M, to shared memory for their columns
@@ -378,26 +398,55 @@ __global__ void __launch_bounds__(kGradBlock, 1)
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int j0 = half * (kC / 2) + 16 * n;
-                float x[16];
+                if (j0 > (i | 31)) {   // above the diagonal for the whole warp
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) cw[16 * n + t] = pw[16 * n + t] = tr[R * kTrLd + j0 + t] = 0.0f;
+                    continue;
+                }
+                float x[16], e[16], be[16];
+                get16(bs + j0, be);
                 tm_ld16(mine + kTmXF + j0, x);
+                if (j0 / 16 < i / 16) {
+                    const float2 Gj = Gs[j0 + 15];
+                    const float r = mul * exp2f((Gi.x - Gj.x) + (Gi.y - Gj.y));
+                    get16(ce + j0, e);
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) x[t] *= r * e[t];
+                } else if (j0 / 16 == i / 16) {
+                    const int m = low ? i : i + 1;
+                    const float r = rf[i];
+                    if (r >= 0.0f) {   // the same for the 16 tokens
+                        get16(de + j0, e);
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) x[t] = j0 + t < m ? x[t] * (mul * r * e[t]) : 0.0f;
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) {
+                            const float2 Gj = Gs[j0 + t];
+                            x[t] = j0 + t < m ? x[t] * mul * exp2f((Gi.x - Gj.x) + (Gi.y - Gj.y)) : 0.0f;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) x[t] = 0.0f;
+                }
 #pragma unroll
                 for (int t = 0; t < 16; ++t) {
-                    const int j = j0 + t;
-                    const float2 Gj = Gs[j];
-                    const bool in = low ? j < i : j <= i;
-                    const float w = in ? x[t] * mul * exp2f((Gi.x - Gj.x) + (Gi.y - Gj.y)) : 0.0f;
-                    cw[16 * n + t] = w * raw[16 * n + t];
-                    pw[16 * n + t] = j <= i ? rs : 0.0f;   // what this half's columns before j hand to row i >= j
-                    rs = fmaf(bs[j], cw[16 * n + t], rs);
-                    tr[R * kTrLd + j] = bs[j] * w;
+                    cw[16 * n + t] = x[t] * raw[16 * n + t];
+                    pw[16 * n + t] = j0 + t <= i ? rs : 0.0f;   // what this half's columns before j hand to row i >= j
+                    rs = fmaf(be[t], cw[16 * n + t], rs);
+                    tr[R * kTrLd + j0 + t] = be[t] * x[t];
                 }
             }
             if (half == 0) rsum[R] = rs;
-            column_sums(cw, lane);
-            column_sums(pw, lane);
+            if (half * (kC / 2) <= (i | 31)) {   // else zeros
+                column_sums(cw, lane);
+                column_sums(pw, lane);
+            }
             csum[(warp & 3) * kC + half * (kC / 2) + lane] = cw[0];
             gsum[(warp & 3) * kC + half * (kC / 2) + lane] = pw[0];
         }
+        get_state<DKT, DVT>(f, 0, ud, a.dk, a.dv, tid);
         wait2();   // the left operand and S0 are used up
         if (low) {   // E as left operand (rows 64-127 of the product go unread)
 #pragma unroll
@@ -413,7 +462,11 @@ __global__ void __launch_bounds__(kGradBlock, 1)
                 }
             }
         }
-        float both = put_state<DKT, DVT, true>(smem, L::kS, ud, a.dk, a.dv, tid);   // <S0, dS1>
+        float both = put_state<DKT, DVT, true>(smem, L::kS, f, 0, tid);   // <S0, dS1>
+        if constexpr (DVT * DKT / 8 > 4 * kGradThreads) {
+            get_state<DKT, DVT>(f, 1, ud, a.dk, a.dv, tid);
+            both += put_state<DKT, DVT, true>(smem, L::kS, f, 1, tid);
+        }
 #pragma unroll
         for (int o = 16; o; o >>= 1) both += __shfl_xor_sync(0xffffffffu, both, o);
         if (lane == 0) red[warp] = both;

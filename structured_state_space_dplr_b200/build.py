@@ -22,7 +22,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libs4dplr.so")
 SOURCES = ["api.cu", "cauchy.cu", "kgen.cu", "spectral.cu", "quad.cu", "quad_spec.cu", "s4d.cu", "decode.cu", "noalloc.cu", "backward.cu", "block.cu", "zoh_dplr.cu",
            "api_mixer.cu", "norm.cu", "delta_scan.cu", "delta_prep.cu",
-           "delta_chunk.cu", "delta_back.cu", "delta_grad.cu"]
+           "delta_chunk.cu", "delta_back.cu", "delta_grad.cu",
+           "delta_join.cu"]
 HEADERS = ["common.cuh", "fft.cuh", "cauchy.cuh", "pairs.cuh", "cluster.cuh", "quad.cuh", "launch.h", "umma.cuh", "dtype.cuh", "delta.cuh"]
 
 NVCC_FLAGS = [

@@ -89,7 +89,7 @@ DeltaWork delta_work(int dtype, int Bt, long long tokens, int Hk, int Hv, int Dk
     w.state = keep ? (size_t)units * Dk * Dv * 4 : 0;
     w.rows = keep ? (size_t)units * 64 * Dv * 4 : 0;
     w.seg = s4::delta_segment(tokens, Bt, Hv);
-    w.sums = s4::delta_segment_bytes(tokens, Bt, Hv, Dk, Dv, w.seg);
+    w.sums = s4::delta_segment_bytes(tokens, Bt, Hv, Dk, Dv, w.seg, keep);
     w.total = w.prep + 2 * w.state + 2 * w.rows + w.sums;
     return w;
 }
@@ -279,12 +279,12 @@ s4_status s4_gated_delta_backward(s4_dtype dtype, const float *g, const float *b
         return S4_ERR_INVALID_ARG;
     s4::DeltaArgs a{};
     a.g = g, a.beta = beta, a.n = Bt, a.hk = Hk, a.hv = Hv, a.dk = Dk, a.dv = Dv, a.scale = scale;
-    a.cu = cu_seqlens, a.t = cu_seqlens ? 0 : (int)(tokens / Bt), a.tokens = tokens;
+    a.cu = cu_seqlens, a.t = cu_seqlens ? 0 : (int)(tokens / Bt), a.tokens = tokens, a.seg = w.seg;
     char *p = (char *)workspace + w.prep;
     float *ks = (float *)p, *ke = (float *)(p + w.state), *kds = (float *)(p + w.state + w.rows),
           *kdr = (float *)(p + 2 * w.state + w.rows);
     s = cuda_status(s4::launch_delta_backward(dtype, a, d_o, d_final_state, d_initial_state, workspace, dv, kds, kdr,
-                                              d_flags, stream));
+                                              p + 2 * w.state + 2 * w.rows, d_flags, stream));
     if (s != S4_OK || tokens == 0) return s;
     return cuda_status(
         s4::launch_delta_gradient(dtype, a, d_o, workspace, ks, ke, kds, kdr, dq, dk, dg, dbeta, d_flags, stream));

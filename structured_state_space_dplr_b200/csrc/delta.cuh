@@ -109,6 +109,24 @@ __device__ __forceinline__ Segment segment_of(const DeltaArgs &a, long long numb
     return r;
 }
 
+// What is kept of segments, all in float: for each segment and value head N
+// [dk][dv] and M [dk][dk] by columns (a segment takes the state S to M S + N),
+// and the state before it; with `keep`, for the backward pass, M by rows, the
+// gradient dN [dk][dv] (the state's gradient goes back as M^T dS + dN) and the
+// state's gradient behind it.
+struct Summaries {
+    size_t dd, dv;   // floats of M and of a state
+    bool keep;
+    __host__ __device__ Summaries(int dk, int dv_, bool keep_) : dd((size_t)dk * dk), dv((size_t)dk * dv_), keep(keep_) {}
+    __host__ __device__ size_t unit() const { return 2 * dv + dd + (keep ? dd + 2 * dv : 0); }
+    __host__ __device__ float *n(float *p, size_t u) const { return p + u * unit(); }
+    __host__ __device__ float *m(float *p, size_t u) const { return n(p, u) + dv; }
+    __host__ __device__ float *start(float *p, size_t u) const { return m(p, u) + dd; }
+    __host__ __device__ float *m_rows(float *p, size_t u) const { return start(p, u) + dv; }
+    __host__ __device__ float *dn(float *p, size_t u) const { return m_rows(p, u) + dd; }
+    __host__ __device__ float *behind(float *p, size_t u) const { return dn(p, u) + dv; }
+};
+
 // the chunk that owns a slot: its first token and its tokens (0: none)
 struct Chunk {
     long long tok;

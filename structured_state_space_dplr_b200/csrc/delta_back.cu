@@ -29,9 +29,11 @@ constexpr int kTmS = 0, kTmSl = 128, kTmK = 192, kTmR = 256, kTmX = 320, kTmKl =
 
 enum { bFull = 0, bEmpty = 2, bS = 4, bK = 8, bR = 10, bX = 12, bY, bM1, bMx, bM2, bM3, bCount };
 
-template <typename T, int DKT>
+// SUM: dN of a segment, the state's gradient before it from none behind it,
+// without output. Otherwise the segment itself, from the gradient behind it.
+template <typename T, int DKT, bool SUM>
 __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, const T *dout, const float *dlast,
-                                                                float *dinit, const unsigned char *ws,
+                                                                float *dinit, float *sums, const unsigned char *ws,
                                                                 const unsigned char *images, T *dv, float *keep_ds,
                                                                 float *keep_dr, unsigned *flags) {
     using L = Stage<T, DKT>;
@@ -41,9 +43,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + ST * stage_bytes);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + bCount);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-    const int hv = blockIdx.x % a.hv, s = blockIdx.x / a.hv, hk = hv / (a.hv / a.hk);
-    const Seq sq = sequence(a, s);
-    const int chunks = uniform((sq.len + kC - 1) / kC);
+    const int hv = blockIdx.x % a.hv, hk = hv / (a.hv / a.hk);
+    const Segment sg = segment_of(a, blockIdx.x / a.hv);
+    if (sg.s < 0 || (SUM && sg.index == 0)) return;
+    const Summaries su(a.dk, a.dv, true);
+    Seq sq = sequence(a, sg.s);   // from here on the segment as a sequence
+    sq.tok0 += (long long)sg.first * kC;
+    sq.slot0 += sg.first;
+    sq.len = sq.len - sg.first * kC < sg.chunks * kC ? sq.len - sg.first * kC : sg.chunks * kC;
+    const int chunks = uniform(sg.chunks);
     const long long orow = (long long)a.hv * a.dv;   // dO and dV are contiguous
 
     if (warp == 0) umma::tmem_alloc(tslot, 512);
@@ -198,11 +206,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
         const uint32_t mine = tm + ((uint32_t)((warp & 3) * 32) << 16);
         const bool vin = v < a.dv;
         float S[HC];
-        const size_t st0 = ((size_t)s * a.hv + hv) * a.dk * a.dv + v;
+        const size_t st0 = ((size_t)sg.s * a.hv + hv) * a.dk * a.dv + v;
+        const float *from = SUM ? nullptr : a.seg ? su.behind(sums, blockIdx.x) + v : dlast ? dlast + st0 : nullptr;
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
             const int d = h * HC + i;
-            S[i] = dlast && vin && d < a.dk ? __ldg(dlast + st0 + (size_t)d * a.dv) : 0.0f;
+            S[i] = from && vin && d < a.dk ? __ldg(from + (size_t)d * a.dv) : 0.0f;
         }
         auto done = [&](int bar) {   // this warp's tensor-memory writes (and reads) before the barrier
             tm_wait_st();
@@ -225,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 tm_split16(mine + kTmS + 16 * (h * NS + m), mine + kTmSl + 8 * (h * NS + m), x);
                 done(bS + m);
             }
-            if (vin) store_state<HC>(keep_ds + (size_t)unit * a.dk * a.dv, S, h, v, a.dk, a.dv);
+            if (!SUM && vin) store_state<HC>(keep_ds + (size_t)unit * a.dk * a.dv, S, h, v, a.dk, a.dv);
             ok = umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit);
             if (!ok) break;
 #pragma unroll
@@ -278,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 for (int j = 0; j < 16; ++j) y[j] = -e[j] * x[j];
                 tm_split16(mine + kTmR + j0, mine + kTmRl + j0 / 2, y);
                 done(bR + m);
+                if (SUM) continue;
                 if (vin) store_tokens(keep_dr + (size_t)unit * kC * a.dv, x, j0, v);
                 store16<T>(dv + (sq.tok0 + (long long)c * kC + j0) * orow + (long long)hv * a.dv + v, orow, x, lane, vin,
                            rows - j0);
@@ -300,10 +310,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 ++turn;
             }
         }
-        if (dinit && vin) {
+        float *to = SUM ? su.dn(sums, blockIdx.x) + v : dinit && sg.index == 0 ? dinit + st0 : nullptr;
+        if (to && vin) {
 #pragma unroll
             for (int i = 0; i < HC; ++i)
-                if (h * HC + i < a.dk) dinit[st0 + (size_t)(h * HC + i) * a.dv] = S[i];
+                if (h * HC + i < a.dk) to[(size_t)(h * HC + i) * a.dv] = S[i];
         }
     }
     if (!ok && flags && lane == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
@@ -321,32 +332,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
 
 template <typename T, int DKT>
 cudaError_t run(const DeltaArgs &a, const void *dout, const float *dlast, float *dinit, const void *ws, void *dv,
-                float *keep_ds, float *keep_dr, unsigned *flags, cudaStream_t st) {
+                float *keep_ds, float *keep_dr, void *summaries, unsigned *flags, cudaStream_t st) {
     const int smem = Stage<T, DKT>::count(a.dv) * Stage<T, DKT>::bytes(a.dv) + 256;
-    static SmemLimit limit;
-    cudaError_t e = limit.raise(k_delta_backward<T, DKT>, smem);
+    static SmemLimit limit, limit_sum;
+    cudaError_t e = limit.raise(k_delta_backward<T, DKT, false>, smem);
     if (e != cudaSuccess) return e;
-    const unsigned char *units = (const unsigned char *)ws;
-    k_delta_backward<T, DKT><<<a.n * a.hv, kThreads, smem, st>>>(
-        a, (const T *)dout, dlast, dinit, units, units + (size_t)slots(a.tokens, a.n) * a.hv * kUnitBytes, (T *)dv,
-        keep_ds, keep_dr, flags);
+    const long long chunks = slots(a.tokens, a.n), blocks = segments(chunks, a.n, a.seg) * a.hv;
+    const unsigned char *units = (const unsigned char *)ws, *images = units + (size_t)chunks * a.hv * kUnitBytes;
+    float *sums = (float *)summaries;
+    if (a.seg) {
+        e = limit_sum.raise(k_delta_backward<T, DKT, true>, smem);
+        if (e != cudaSuccess) return e;
+        k_delta_backward<T, DKT, true><<<(unsigned)blocks, kThreads, smem, st>>>(
+            a, (const T *)dout, nullptr, nullptr, sums, units, images, nullptr, nullptr, nullptr, flags);
+        e = launch_delta_join(a, dlast, sums, true, true, flags, st);
+        if (e != cudaSuccess) return e;
+    }
+    k_delta_backward<T, DKT, false><<<(unsigned)blocks, kThreads, smem, st>>>(
+        a, (const T *)dout, dlast, dinit, sums, units, images, (T *)dv, keep_ds, keep_dr, flags);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_delta_backward(int dtype, const DeltaArgs &a, const void *dout, const float *dlast, float *dinit,
-                                  const void *ws, void *dv, float *keep_ds, float *keep_dr, unsigned *flags,
-                                  cudaStream_t st) {
+                                  const void *ws, void *dv, float *keep_ds, float *keep_dr, void *summaries,
+                                  unsigned *flags, cudaStream_t st) {
     const bool wide = a.dk > 64;
     if (dtype == S4_BF16)
-        return wide ? run<__nv_bfloat16, 128>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st)
-                    : run<__nv_bfloat16, 64>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st);
+        return wide ? run<__nv_bfloat16, 128>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, summaries, flags, st)
+                    : run<__nv_bfloat16, 64>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, summaries, flags, st);
     if (dtype == S4_F16)
-        return wide ? run<__half, 128>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st)
-                    : run<__half, 64>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st);
-    return wide ? run<float, 128>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st)
-                : run<float, 64>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, flags, st);
+        return wide ? run<__half, 128>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, summaries, flags, st)
+                    : run<__half, 64>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, summaries, flags, st);
+    return wide ? run<float, 128>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, summaries, flags, st)
+                : run<float, 64>(a, dout, dlast, dinit, ws, dv, keep_ds, keep_dr, summaries, flags, st);
 }
 
 }  // namespace s4

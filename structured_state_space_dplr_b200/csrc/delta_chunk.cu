@@ -44,7 +44,7 @@ enum { bFull = 0, bEmpty = 2, bS = 4, bR = 8, bE = 10, bO = 12, bM1, bM2, bMq, b
 // the state that `starts` has for it.
 template <typename T, int DKT, bool SUM>
 __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, const float *init, float *last,
-                                                               float *sums, const float *starts,
+                                                               float *sums, bool keep_m,
                                                                const unsigned char *ws,
                                                                const unsigned char *images, float *keep_s,
                                                                float *keep_e, unsigned *flags) {
@@ -59,7 +59,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
     const bool ident = SUM && (blockIdx.x & 1);
     const int hv = block % a.hv, hk = hv / (a.hv / a.hk);
     const Segment sg = segment_of(a, block / a.hv);
-    if (sg.s < 0 || (SUM && sg.last)) return;
+    // not needed: the last segment's N, its M unless for the way back, and the
+    // first one's M where it would meet zeros
+    if (sg.s < 0 || (SUM && sg.last && !(ident && keep_m && sg.index > 0))) return;
+    if (ident && sg.index == 0 && !init) return;
+    const Summaries su(a.dk, a.dv, keep_m);
     Seq sq = sequence(a, sg.s);   // from here on the segment as a sequence
     sq.tok0 += (long long)sg.first * kC;
     sq.slot0 += sg.first;
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
         const long long orow = (long long)a.hv * a.dv;
         float S[HC];
         const size_t st0 = ((size_t)sg.s * a.hv + hv) * a.dk * a.dv + v;
-        const float *from = a.seg ? starts + (size_t)block * a.dk * a.dv + v : init ? init + st0 : nullptr;
+        const float *from = a.seg ? su.start(sums, block) + v : init ? init + st0 : nullptr;
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
             const int d = h * HC + i;
@@ -341,12 +345,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
             }
         }
         if constexpr (SUM) {
-            // N [dk][dv], then M by columns [dk][dk]
-            float *to = sums + (size_t)block * a.dk * (a.dv + a.dk) + (ident ? a.dk * a.dv + v * a.dk : v);
+            float *to = ident ? su.m(sums, block) + (size_t)v * a.dk : su.n(sums, block) + v;
+            float *rows = ident && keep_m ? su.m_rows(sums, block) + v : nullptr;
             if (vin)
 #pragma unroll
                 for (int i = 0; i < HC; ++i)
-                    if (h * HC + i < a.dk) to[(size_t)(h * HC + i) * (ident ? 1 : a.dv)] = S[i];
+                    if (h * HC + i < a.dk) {
+                        to[(size_t)(h * HC + i) * (ident ? 1 : a.dv)] = S[i];
+                        if (rows) rows[(size_t)(h * HC + i) * a.dk] = S[i];
+                    }
         } else {
             if (ok && chunks) put_output(chunks - 1, before);
             if (last && sg.last && vin) {
@@ -369,81 +376,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
     if (warp == 0) umma::tmem_dealloc(tm, 512);
 }
 
-// The states before the segments: S <- M S + N from segment to segment. A block
-// has 16 columns of one sequence's and head's state in shared memory, a thread
-// one row of the result and 8 of the columns; M [dk][dk] by columns comes into
-// shared memory one segment ahead (read from L2 in the loop a segment took
-// 11 us).
-constexpr int kJoinCols = 16;
-__global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, const float *init, const float *sums, float *starts,
-                                                    unsigned *flags) {
-    extern __shared__ __align__(128) float Ms[];   // [2][dk][dk]
-    __shared__ float S[128][kJoinCols];
-    __shared__ uint64_t full[2];
-    const int hv = blockIdx.x % a.hv, s = blockIdx.x / a.hv, v0 = blockIdx.y * kJoinCols;
-    const int d = threadIdx.x & 127, c0 = (threadIdx.x >> 7) * 8, mm = a.dk * a.dk;
-    const int all = (sequence(a, s).len + kC - 1) / kC, n = (all + a.seg - 1) / a.seg;
-    const long long first = segment0(a, s);
-    const bool in = d < a.dk && v0 + c0 < a.dv;   // dv is a multiple of 8
-    auto summary = [&](int g) { return sums + (size_t)((first + g) * a.hv + hv) * a.dk * (a.dv + a.dk); };
-    auto fetch = [&](int g) {   // by one thread
-        umma::fence_proxy_async();
-        mbar_expect(full + (g & 1), mm * 4);
-        bulk_load(Ms + (g & 1) * mm, summary(g) + (size_t)a.dk * a.dv, mm * 4, full + (g & 1));
-        mbar_arrive(full + (g & 1));
-    };
-    if (threadIdx.x == 0) {
-        umma::mbar_init(full, 1);
-        umma::mbar_init(full + 1, 1);
-        umma::fence_mbar_init();
-        if (n > 1) fetch(0);
-    }
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        x[j] = in && init ? __ldg(init + (((size_t)s * a.hv + hv) * a.dk + d) * a.dv + v0 + c0 + j) : 0.0f;
-    bool ok = true;
-    for (int g = 0;; ++g) {
-        if (in) {
-            float4 *to = reinterpret_cast<float4 *>(starts + ((size_t)((first + g) * a.hv + hv) * a.dk + d) * a.dv + v0 + c0);
-            to[0] = make_float4(x[0], x[1], x[2], x[3]);
-            to[1] = make_float4(x[4], x[5], x[6], x[7]);
-        }
-        if (g + 1 >= n) break;
-        float4 p, q;
-        if (in) {
-            const float4 *np = reinterpret_cast<const float4 *>(summary(g) + (size_t)d * a.dv + v0 + c0);
-            p = __ldg(np);
-            q = __ldg(np + 1);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) S[d][c0 + j] = x[j];
-        __syncthreads();   // S is there; the other half of Ms is used up
-        if (threadIdx.x == 0 && g + 2 < n) fetch(g + 1);
-        ok = umma::mbar_wait(full + (g & 1), (g >> 1) & 1, kSpinLimit) && ok;
-        if (in) {
-            x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
-            const float *M = Ms + (g & 1) * mm + d;
-#pragma unroll 8
-            for (int c = 0; c < a.dk; ++c) {
-                const float m = M[c * a.dk];
-                const float4 u = *reinterpret_cast<const float4 *>(&S[c][c0]);
-                const float4 w = *reinterpret_cast<const float4 *>(&S[c][c0 + 4]);
-                x[0] = fmaf(m, u.x, x[0]);
-                x[1] = fmaf(m, u.y, x[1]);
-                x[2] = fmaf(m, u.z, x[2]);
-                x[3] = fmaf(m, u.w, x[3]);
-                x[4] = fmaf(m, w.x, x[4]);
-                x[5] = fmaf(m, w.y, x[5]);
-                x[6] = fmaf(m, w.z, x[6]);
-                x[7] = fmaf(m, w.w, x[7]);
-            }
-        }
-        __syncthreads();
-    }
-    if (!ok && flags && threadIdx.x == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
-}
-
 template <typename T, int DKT>
 cudaError_t run(const DeltaArgs &a, const float *init, float *last, const void *ws, float *keep_s, float *keep_e,
                 void *summaries, unsigned *flags, cudaStream_t st) {
@@ -453,19 +385,17 @@ cudaError_t run(const DeltaArgs &a, const float *init, float *last, const void *
     if (e != cudaSuccess) return e;
     const long long chunks = slots(a.tokens, a.n), blocks = segments(chunks, a.n, a.seg) * a.hv;
     const unsigned char *units = (const unsigned char *)ws, *images = units + (size_t)chunks * a.hv * kUnitBytes;
-    float *sums = (float *)summaries, *starts = sums + (size_t)blocks * a.dk * (a.dk + a.dv);
+    float *sums = (float *)summaries;
+    const bool keep = keep_s != nullptr;
     if (a.seg) {
         e = limit_sum.raise(k_delta_forward<T, DKT, true>, smem);
         if (e != cudaSuccess) return e;
-        k_delta_forward<T, DKT, true><<<(unsigned)(2 * blocks), kThreads, smem, st>>>(a, init, nullptr, sums, nullptr, units,
+        k_delta_forward<T, DKT, true><<<(unsigned)(2 * blocks), kThreads, smem, st>>>(a, init, nullptr, sums, keep, units,
                                                                                     images, nullptr, nullptr, flags);
-        static SmemLimit limit_join;
-        e = limit_join.raise(k_delta_join, 2 * 128 * 128 * sizeof(float));
+        e = launch_delta_join(a, init, sums, keep, false, flags, st);
         if (e != cudaSuccess) return e;
-        k_delta_join<<<dim3(a.n * a.hv, (a.dv + kJoinCols - 1) / kJoinCols), 256, 2 * a.dk * a.dk * sizeof(float), st>>>(
-            a, init, sums, starts, flags);
     }
-    k_delta_forward<T, DKT, false><<<(unsigned)blocks, kThreads, smem, st>>>(a, init, last, nullptr, starts, units, images,
+    k_delta_forward<T, DKT, false><<<(unsigned)blocks, kThreads, smem, st>>>(a, init, last, sums, keep, units, images,
                                                                             keep_s, keep_e, flags);
     return cudaGetLastError();
 }
@@ -494,8 +424,8 @@ int delta_segment(long long tokens, int n, int hv) {
     return seg;
 }
 
-size_t delta_segment_bytes(long long tokens, int n, int hv, int dk, int dv, int seg) {
-    return seg ? (size_t)segments(slots(tokens, n), n, seg) * hv * dk * (dk + 2 * (size_t)dv) * sizeof(float) : 0;
+size_t delta_segment_bytes(long long tokens, int n, int hv, int dk, int dv, int seg, bool keep) {
+    return seg ? (size_t)segments(slots(tokens, n), n, seg) * hv * Summaries(dk, dv, keep).unit() * sizeof(float) : 0;
 }
 
 cudaError_t launch_delta_forward(int dtype, const DeltaArgs &a, const float *init, float *last, const void *ws,

@@ -135,12 +135,15 @@ cudaError_t launch_delta_forward(int dtype, const DeltaArgs &a, const float *ini
                                  float *keep_s, float *keep_e, void *summaries, unsigned *flags, cudaStream_t st);
 // whether splitting pays: chunks of a segment, or 0
 int delta_segment(long long tokens, int n, int hv);
-size_t delta_segment_bytes(long long tokens, int n, int hv, int dk, int dv, int seg);
+size_t delta_segment_bytes(long long tokens, int n, int hv, int dk, int dv, int seg, bool keep);
+// the states before the segments from init; back: the states' gradients behind them from init
+cudaError_t launch_delta_join(const DeltaArgs &a, const float *init, float *sums, bool keep, bool back, unsigned *flags,
+                              cudaStream_t st);
 
 // backward in the states: dV, the first states' gradient, keep_ds and keep_dr (behind every chunk, of every chunk)
 cudaError_t launch_delta_backward(int dtype, const DeltaArgs &a, const void *dout, const float *dlast, float *dinit,
-                                  const void *ws, void *dv, float *keep_ds, float *keep_dr, unsigned *flags,
-                                  cudaStream_t st);
+                                  const void *ws, void *dv, float *keep_ds, float *keep_dr, void *summaries,
+                                  unsigned *flags, cudaStream_t st);
 // the other gradients, from all that was kept
 cudaError_t launch_delta_gradient(int dtype, const DeltaArgs &a, const void *dout, const void *ws, const float *keep_s,
                                   const float *keep_e, const float *keep_ds, const float *keep_dr, void *dq, void *dk,

@@ -317,3 +317,19 @@ def test_refusals():
         s4.gated_delta_forward(*(e[n] for n in NAMES))                       # Dk not a multiple of 8
     with pytest.raises(s4.S4Error):
         s4.gated_delta_scan(*(e[n] for n in NAMES), e["state"])
+
+
+@pytest.mark.parametrize("shape", [(1, 1500, 1, 2, 64, 64), (2, 2000, 1, 1, 40, 128)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_few_long_sequences_backward(shape, dtype):
+    torch = torch_cuda()
+    d = make(*shape, dtype=dtype)
+    d["g"] *= 0.02
+    do = torch.randn(d["v"].shape, device="cuda", generator=gen(1)).to(d["v"].dtype)
+    ds = torch.randn(d["state"].shape, device="cuda", generator=gen(2))
+    _, _, ref = delta.gated_delta(*(f64(d[n]) for n in NAMES), 0.3, f64(d["state"]), do=f64(do), dstate=f64(ds))
+    _, _, work = forward(d, scale=0.3, initial_state=d["state"], keep=True)
+    for _ in range(2):
+        got = backward(d, do, work, scale=0.3, dfinal_state=ds)
+        for m in (*NAMES, "initial_state"):      # one more chain and the joins, both ways
+            check(got[m], ref[m], got[m].dtype, "d" + m, 4)

@@ -107,24 +107,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                        idesc(16, false, true), acc);
             };
             ok = umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit);
+            // D1 = dS1^T K^T, steps m and NS + m; the orders of the parts' products as in the forward chain
+            auto state_times = [&](int m, int most, int least) {
 #pragma unroll
-            for (int m = 0; m < NS; ++m) {   // D1 = dS1^T K^T, steps m and NS + m
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int o = most; o >= least; --o)
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) {
+                            if (o - j < 0) continue;
+                            const int ks = h * NS + m, p = o - j;
+                            mma_ts(tm + kTmK, tm + (p < 2 ? kTmS + 16 * ks + 8 * p : kTmSl + 8 * ks),
+                                   desc_k(k0 + j * L::kImg + ks * 4096, 2048, 128), idesc(kC, false, false),
+                                   m + h > 0 || o < 2 || j > 0);
+                        }
+            };
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {
                 ok = ok && umma::mbar_wait(bars + bS + m, pn, kSpinLimit);
                 umma::fence_after_sync();
                 if (ok && elect()) {
+                    state_times(m, 2, 1);
+                    if (m == NS - 1) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int o = 2; o >= 0; --o)
-#pragma unroll
-                            for (int j = 0; j < NB; ++j) {
-                                if (o - j < 0) continue;
-                                const int ks = h * NS + m, p = o - j;
-                                mma_ts(tm + kTmK, tm + (p < 2 ? kTmS + 16 * ks + 8 * p : kTmSl + 8 * ks),
-                                       desc_k(k0 + j * L::kImg + ks * 4096, 2048, 128), idesc(kC, false, false),
-                                       m + h > 0 || o < 2 || j > 0);
-                            }
-                    if (m == NS - 1) umma::commit(bars + bM1);
+                        for (int i = 0; i < NS; ++i) state_times(i, 0, 0);
+                        umma::commit(bars + bM1);
+                    }
                 }
                 __syncwarp();
             }
@@ -133,11 +141,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
             umma::fence_after_sync();
             if (ok && elect()) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
+                for (int o = 2; o >= 0; --o)
 #pragma unroll
-                    for (int ib = 3; ib >= ks; --ib)
+                    for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-                        for (int o = 2; o >= 0; --o)
+                        for (int ib = 3; ib >= ks; --ib)
 #pragma unroll
                             for (int p = 0; p < NB; ++p)
                                 if (o - p >= 0) t_times(kTmX, kTmXl, p, ib, o - p, 1, ks, ib < 3 || o < 2 || p > 0);
@@ -150,22 +158,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 ok = ok && umma::mbar_wait(bars + bK + m, pn, kSpinLimit);
                 umma::fence_after_sync();
                 if (ok && elect()) {
+                    auto group = [&](int first, int most, int least) {
 #pragma unroll
-                    for (int ib = m; ib < 4; ib += 2)
+                        for (int o = most; o >= least; --o)
 #pragma unroll
-                        for (int ks = 0; ks <= ib; ++ks)
+                            for (int ib = first; ib < 4; ib += 2)
 #pragma unroll
-                            for (int o = 2; o >= 0; --o)
+                                for (int ks = 0; ks <= ib; ++ks)
 #pragma unroll
-                                for (int p = 0; p <= o; ++p) t_times(kTmK, kTmKl, p, ib, o - p, 0, ks, true);
+                                    for (int p = 0; p <= o; ++p) t_times(kTmK, kTmKl, p, ib, o - p, 0, ks, true);
+                    };
+                    group(m, 2, 1);
+                    if (m == 1) {
+                        group(0, 0, 0);
+                        group(1, 0, 0);
+                    }
                     if (m == 1) umma::commit(bars + bM2);
                 }
                 __syncwarp();
             }
             // D3 = (scale e^G dO)^T Q - (e^G dR)^T K, in the place of the state gradient's parts
-            auto tok_times = [&](uint32_t at, uint32_t low, int row0, int ks, bool first) {
+            auto tok_times = [&](uint32_t at, uint32_t low, int row0, int ks, bool first, int most, int least) {
 #pragma unroll
-                for (int o = 2; o >= 0; --o)
+                for (int o = most; o >= least; --o)
 #pragma unroll
                     for (int j = 0; j < NB; ++j) {
                         if (o - j < 0) continue;
@@ -179,16 +194,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
             umma::fence_after_sync();
             if (ok && elect())
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) tok_times(kTmX, kTmXl, kC, ks, ks == 0);
+                for (int ks = 0; ks < 4; ++ks) tok_times(kTmX, kTmXl, kC, ks, ks == 0, 2, 1);
             __syncwarp();
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 ok = ok && umma::mbar_wait(bars + bR + m, pn, kSpinLimit);
                 umma::fence_after_sync();
                 if (ok && elect()) {
-                    tok_times(kTmR, kTmRl, 0, m, false);
-                    tok_times(kTmR, kTmRl, 0, 2 + m, false);
+                    tok_times(kTmR, kTmRl, 0, m, false, 2, 1);
+                    tok_times(kTmR, kTmRl, 0, 2 + m, false, 2, 1);
                     if (m == 1) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tok_times(kTmX, kTmXl, kC, ks, false, 0, 0);
+                            tok_times(kTmR, kTmRl, 0, ks, false, 0, 0);
+                        }
                         umma::commit(bars + bM3);
                         umma::commit(bars + bEmpty + st);
                     }

@@ -112,19 +112,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
     } else if (warp == kEpiWarps) {
         // ----------------------------------------------------- products ----
         // A K step's products start as soon as the threads have written its
-        // parts; within a step the smallest parts' products come first. What
-        // the next step waits for goes first, Q's and PT's products into the
-        // gaps.
+        // parts. What the next step waits for goes first, Q's and PT's products
+        // into the gaps.
         const uint32_t base = saddr(smem);
         for (int c = 0, st = 0, turn = 0; c < chunks && ok; ++c) {
             const int pc = c & 1;
             const uint32_t k0 = base + st * stage_bytes, t0 = k0 + L::kTp;
+            // Of every product the orders from `most` to `least` (2: the smallest
+            // parts' products). The accumulators round down with every
+            // addition, so the largest products come last of all steps.
             // S0^T K^T (row0 = 0) or S0^T Q^T (64): steps n and NS + n
-            auto state_times = [&](uint32_t d, int row0, int n) {
+            auto state_times = [&](uint32_t d, int row0, int n, int most, int least) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int o = 2; o >= 0; --o)
+                    for (int o = most; o >= least; --o)
 #pragma unroll
                         for (int j = 0; j < NB; ++j) {
                             if (o - j < 0) continue;
@@ -135,17 +137,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                         }
             };
             // R^T T^T (pt = 0) or R^T PT^T (1): steps n and 2 + n, which meet rows 16 ks and up
-            auto r_times = [&](uint32_t d, int pt, int n) {
+            auto r_times = [&](uint32_t d, int pt, int n, int most, int least) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int o = 2; o >= 0; --o)
+                    for (int o = most; o >= least; --o)
 #pragma unroll
                         for (int j = 0; j <= o; ++j) {
                             const int ks = 2 * h + n, p = o - j;
                             mma_ts(tm + d + 16 * ks, tm + (p < 2 ? kTmK + 16 * ks + 8 * p : kTmRl + 8 * ks),
                                    desc_k(t0 + j * kTpImage + tp_offset(ks) + pt * tp_rows(ks), tp_group(ks), 128),
                                    idesc(kC - 16 * ks, false, false), n + h > 0 || o < 2 || j > 0);
+                        }
+            };
+            // D3 = (beta e^(G_C - G) E)^T K, in the place of the state's parts
+            auto e_times = [&](int n, int most, int least) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int o = most; o >= least; --o)
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) {
+                            if (o - j < 0) continue;
+                            const int ks = 2 * h + n, p = o - j;
+                            mma_ts(tm + kTmS, tm + (p < 2 ? kTmE + 16 * ks + 8 * p : kTmEl + 8 * ks),
+                                   desc_mn(k0 + j * L::kImg + ks * 256, 128, 2048), idesc(DKT, false, true),
+                                   n + h > 0 || o < 2 || j > 0);
                         }
             };
             ok = umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit) &&
@@ -155,8 +172,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 ok = ok && umma::mbar_wait(bars + bS + n, pc, kSpinLimit);
                 umma::fence_after_sync();
                 if (ok && elect()) {
-                    state_times(kTmK, 0, n);
-                    if (n == NS - 1) umma::commit(bars + bM1);
+                    state_times(kTmK, 0, n, 2, 1);
+                    if (n == NS - 1) {
+#pragma unroll
+                        for (int i = 0; i < NS; ++i) state_times(kTmK, 0, i, 0, 0);
+                        umma::commit(bars + bM1);
+                    }
                 }
                 __syncwarp();
             }
@@ -165,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 umma::fence_after_sync();
                 if (ok && elect())
 #pragma unroll
-                    for (int n = 0; n < NS / 2; ++n) state_times(kTmQ, kC, n);
+                    for (int n = 0; n < NS; ++n) state_times(kTmQ, kC, n, 2, NB == 1 ? 2 : 1);
                 __syncwarp();
             }
 #pragma unroll
@@ -173,42 +194,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 ok = ok && umma::mbar_wait(bars + bR + n, pc, kSpinLimit);
                 umma::fence_after_sync();
                 if (ok && elect()) {
-                    r_times(kTmE, 0, n);
+                    r_times(kTmE, 0, n, 2, 1);
                     if (n == 1) {
+                        r_times(kTmE, 0, 0, 0, 0);
+                        r_times(kTmE, 0, 1, 0, 0);
                         umma::commit(bars + bM2);
                         if constexpr (!SUM) {
+                            if (NB == 1)
 #pragma unroll
-                            for (int i = NS / 2; i < NS; ++i) state_times(kTmQ, kC, i);
+                                for (int i = 0; i < NS; ++i) state_times(kTmQ, kC, i, 1, 1);
+#pragma unroll
+                            for (int i = 0; i < NS; ++i) state_times(kTmQ, kC, i, 0, 0);
                         }
                         umma::commit(bars + bMq);
                     }
                 }
                 __syncwarp();
             }
-            // D3 = (beta e^(G_C - G) E)^T K, in the place of the state's parts
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 ok = ok && umma::mbar_wait(bars + bE + n, pc, kSpinLimit);
                 if (n == 0) ok = ok && umma::mbar_wait(bars + bMq, pc, kSpinLimit);   // the state's parts have been read
                 umma::fence_after_sync();
                 if (ok && elect()) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int o = 2; o >= 0; --o)
-#pragma unroll
-                            for (int j = 0; j < NB; ++j) {
-                                if (o - j < 0) continue;
-                                const int ks = 2 * h + n, p = o - j;
-                                mma_ts(tm + kTmS, tm + (p < 2 ? kTmE + 16 * ks + 8 * p : kTmEl + 8 * ks),
-                                       desc_mn(k0 + j * L::kImg + ks * 256, 128, 2048), idesc(DKT, false, true),
-                                       n + h > 0 || o < 2 || j > 0);
-                            }
+                    e_times(n, 2, 1);
                     if (n == 1) {
+                        e_times(0, 0, 0);
+                        e_times(1, 0, 0);
                         umma::commit(bars + bM3);
                         if constexpr (!SUM) {
-                            r_times(kTmO, 1, 0);
-                            r_times(kTmO, 1, 1);
+                            r_times(kTmO, 1, 0, 2, 1);
+                            r_times(kTmO, 1, 1, 2, 1);
+                            r_times(kTmO, 1, 0, 0, 0);
+                            r_times(kTmO, 1, 1, 0, 0);
                         }
                         umma::commit(bars + bM2o);
                         umma::commit(bars + bEmpty + st);

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 umma::fence_after_sync();
                 if (ok && elect())
 #pragma unroll
-                    for (int n = 0; n < NS; ++n) state_times(kTmQ, kC, n, 2, NB == 1 ? 2 : 1);
+                    for (int n = 0; n < NS; ++n) state_times(kTmQ, kC, n, 2, 1);
                 __syncwarp();
             }
 #pragma unroll
@@ -200,9 +200,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                         r_times(kTmE, 0, 1, 0, 0);
                         umma::commit(bars + bM2);
                         if constexpr (!SUM) {
-                            if (NB == 1)
-#pragma unroll
-                                for (int i = 0; i < NS; ++i) state_times(kTmQ, kC, i, 1, 1);
 #pragma unroll
                             for (int i = 0; i < NS; ++i) state_times(kTmQ, kC, i, 0, 0);
                         }

@@ -41,10 +41,13 @@ template <typename T, int DKT, int DVT>
 struct GradSmem {
     static constexpr int kS = DVT * DKT * 2, kE = kC * DVT * 2, kKq = kq_bytes<T, DKT>();   // one part of S0 or dS1, of E; all of [K; Q]
     static constexpr int kSmall = 2 * kC * kTrLd * 4 + kC * 8 + 22 * kC * 4 + 128;
-    // [K; Q] stays beside the states' image where there is room for both
-    static constexpr bool kBeside = 3 * kS + 3 * kE + kKq + kSmall <= 232448;
-    static constexpr int kArea = kBeside ? 3 * kS + kKq : (3 * kS > kKq ? 3 * kS : kKq);
-    static constexpr int kOffKq = kBeside ? 3 * kS : 0, kOffE = kArea, kOffSmall = kArea + 3 * kE;
+    // The states' image; before them a head's E, dR and dO as they are
+    static constexpr int kRow = DVT * (int)sizeof(T) + 16;   // dO's rows, shifted banks
+    static constexpr int kRaw = 2 * kC * DVT * 4 + kC * kRow, kFirst = 3 * kS > kRaw ? 3 * kS : kRaw;
+    // [K; Q] stays beside it where there is room for both
+    static constexpr bool kBeside = kFirst + 3 * kE + kKq + kSmall <= 232448;
+    static constexpr int kArea = kBeside ? kFirst + kKq : (kFirst > kKq ? kFirst : kKq);
+    static constexpr int kOffKq = kBeside ? kFirst : 0, kOffE = kArea, kOffSmall = kArea + 3 * kE;
     static constexpr int kBytes = kOffSmall + kSmall;
     static_assert(kBytes <= 232448, "shared memory of a block");
 };
@@ -58,11 +61,6 @@ __device__ __forceinline__ void put_parts(unsigned char *dst, int part, const fl
     for (int q = 0; q < 3; ++q)
         *reinterpret_cast<uint4 *>(dst + q * part) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
 }
-__device__ __forceinline__ void get8(const float *p, float (&f)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-
 // sums over the warp: lane l ends with the sum of the lanes' w[l] in w[0]
 __device__ __forceinline__ void column_sums(float (&w)[32], int lane) {
 #pragma unroll
@@ -124,8 +122,13 @@ __device__ __forceinline__ float put_state(unsigned char *dst, int part, const f
     return both;
 }
 
+// 8 elements of shared memory, 16-byte aligned
+__device__ __forceinline__ void take8(const float *p, float (&f)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
 template <typename T>
-__device__ __forceinline__ void get8(const T *p, float (&f)[8]) {   // 16-bit types
+__device__ __forceinline__ void take8(const T *p, float (&f)[8]) {   // 16-bit types
     load_pack<T, 8>(p, f);
 }
 
@@ -147,8 +150,8 @@ __global__ void __launch_bounds__(kGradBlock, 1)
     float *gsum = csum + 4 * kC, *rsum = gsum + 4 * kC;                      // [4][64], [128]
     float *dot = rsum + 2 * kC, *hdot = dot + 4 * kC;                        // [2][128], [2][64]
     float *red = hdot + 2 * kC;                                              // [8]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(red + 8);                  // kq, two products in flight
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 3);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(red + 8);                  // kq, two products in flight, raw
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 4);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int R = (warp & 3) * 32 + lane, i = R & (kC - 1), half = warp >> 2;   // row of [dR; dO] and of [K; Q], its token
     const bool low = R < kC;                                                    // a row of dR and K
@@ -164,6 +167,7 @@ __global__ void __launch_bounds__(kGradBlock, 1)
     if (warp == 0) umma::tmem_alloc(tslot, 512);
     if (tid == 0) {
         for (int n = 0; n < 3; ++n) umma::mbar_init(bars + n, 1);
+        umma::mbar_init(bars + 3, kGradThreads + 1);
         umma::fence_mbar_init();
     }
     umma::fence_before_sync();
@@ -218,22 +222,6 @@ __global__ void __launch_bounds__(kGradBlock, 1)
     constexpr std::integral_constant<int, kC / 16> kKc;
     constexpr std::integral_constant<int, 3> kThree;
     constexpr std::integral_constant<int, NB> kNb;
-    // all that the heads of this block read on its way to L2 (for the block that
-    // follows on the SM as well, it would not all stay there: 1228 us for 1075)
-    if (tid < 4 * per) {
-        const long long unit = slot * a.hv + hk * per + tid / 4;
-        const uint32_t st = (uint32_t)(a.dk * a.dv) * 4, tk = (uint32_t)(kC * a.dv) * 4;
-        switch (tid % 4) {
-            case 0: bulk_prefetch(keep_e + (size_t)unit * kC * a.dv, tk); break;
-            case 1: bulk_prefetch(keep_dr + (size_t)unit * kC * a.dv, tk); break;
-            case 2: bulk_prefetch(keep_s + (size_t)unit * a.dk * a.dv, st); break;
-            default: bulk_prefetch(keep_ds + (size_t)unit * a.dk * a.dv, st); break;
-        }
-    }
-    if (tid < rows)   // dO's rows too, the heads of this block side by side
-        for (int b = 0; b < per * a.dv * (int)sizeof(T); b += 128)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"((const char *)(dout + (tok + tid) * orow + (long long)hk * per * a.dv) + b));
-
     if (warp == kGradWarps) {
         // the products, by a warp of their own: issuing them takes as long as they take
         load_kq();
@@ -255,8 +243,22 @@ __global__ void __launch_bounds__(kGradBlock, 1)
             umma::commit(bars + 1);
         }
         __syncwarp();
+        // E and dR as they are to the place of the states' image, when nobody reads it
+        auto load_raw = [&](int g) {
+            if (elect()) {
+                const long long unit = slot * a.hv + hk * per + g;
+                const uint32_t bytes = (uint32_t)(kC * a.dv) * 4;
+                mbar_expect(bars + 3, 2 * bytes);
+                bulk_load(smem, keep_e + (size_t)unit * kC * a.dv, bytes, bars + 3);
+                bulk_load(smem + kC * DVT * 4, keep_dr + (size_t)unit * kC * a.dv, bytes, bars + 3);
+                mbar_arrive(bars + 3);
+            }
+            __syncwarp();
+        };
+        if (L::kBeside) load_raw(0);
         for (int g = 0; g < per; ++g) {
             barrier();
+            if (!L::kBeside) load_raw(g);
             barrier();
             if (elect()) {
                 times(kKv, kThree, kTmXF, kTmA, kTmA + DVT, desc_k(e0, 1024, 128), L::kE, 2048, idesc(kC, false, false), true);
@@ -277,6 +279,10 @@ __global__ void __launch_bounds__(kGradBlock, 1)
                 umma::commit(bars + 1);
             }
             __syncwarp();
+            if (L::kBeside && g + 1 < per) {
+                ok = umma::mbar_wait(bars + 1, 0, kSpinLimit) && ok;   // the phases' products: q.k, then X F and H in turn
+                load_raw(g + 1);
+            }
             if constexpr (!L::kBeside) {
                 barrier();
                 load_kq();
@@ -307,12 +313,23 @@ __global__ void __launch_bounds__(kGradBlock, 1)
 #pragma unroll
     for (int n = 0; n < HK; ++n) acc[n] = 0.0f;
 
+    auto load_do = [&](int g) {   // dO's rows, padded, zeros behind the last
+        constexpr int E = 16 / (int)sizeof(T), kPer = DVT / E;
+        const T *src = dout + tok * orow + (long long)(hk * per + g) * a.dv;
+        for (int n = tid; n < kC * kPer; n += kGradThreads) {
+            const int r = n / kPer, c = n % kPer;
+            const bool in = r < rows && c * E < a.dv;
+            cp16(smem + 2 * kC * DVT * 4 + r * L::kRow + c * 16, in ? src + r * orow + c * E : dout, in);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(saddr(bars + 3)) : "memory");
+    };
+    if (L::kBeside) load_do(0);
     for (int g = 0; g < per; ++g) {
         const int hv = hk * per + g;
         const long long unit = slot * a.hv + hv;
         const float *us = keep_s + (size_t)unit * a.dk * a.dv, *ud = keep_ds + (size_t)unit * a.dk * a.dv;
-        const float *ue = keep_e + (size_t)unit * kC * a.dv, *ur = keep_dr + (size_t)unit * kC * a.dv;
         barrier();   // the last head's reads of shared and tensor memory
+        if (!L::kBeside) load_do(g);
         if (warp == 1) {
             const GateSums gt = gate_sums(a, tok, hv, rows, lane);
             const int j = 2 * lane;
@@ -337,50 +354,37 @@ __global__ void __launch_bounds__(kGradBlock, 1)
             de[j] = exp2f((float)(near ? first - gt.x : 0.0));
             de[j + 1] = exp2f((float)(near ? first - gt.y : 0.0));
         }
-        // E as right operand (rows tokens, K = v) and [dR; dO] as left operand
-        // (half of the columns a thread); one's loads beside the other's parts
-        auto get_x = [&](float (&f)[4][8], int n0) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int v = half * (DVT / 2) + 8 * (n0 + n);
-                zero8(f[n]);
-                if (v < a.dv) {
-                    if (low)
-                        get8(ur + ((size_t)(v >> 3) * kC + i) * 8, f[n]);
-                    else if (i < rows)
-                        get8(dout + (tok + i) * orow + (long long)hv * a.dv + v, f[n]);
-                }
-            }
-        };
-        auto put_x = [&](const float (&f)[4][8], int n0) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int ks = half * (KV / 2) + n0 / 2 + n;
-                float x[16];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = f[2 * n][j], x[8 + j] = f[2 * n + 1][j];
-                tm_split16(mine + kTmA + 16 * ks, mine + kTmA + DVT + 8 * ks, x);
-            }
-        };
         float f[4][8];
-        {
-            float fx[4][8];
-            get_x(fx, 0);
+        get_state<DKT, DVT>(f, 0, us, a.dk, a.dv, tid);   // on its way
+        ok = umma::mbar_wait(bars + 3, g & 1, kSpinLimit) && ok;
+        // E as right operand (rows tokens, K = v)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int n = u * kGradThreads + tid;
-                zero8(f[u]);
-                if (n < kC * DVT / 8 && 8 * (n / kC) < a.dv) get8(ue + (size_t)n * 8, f[u]);
-            }
-            put_x(fx, 0);
-            if constexpr (KV > 4) get_x(fx, 4);
+        for (int u = 0; u < kC * DVT / 8 / kGradThreads; ++u) {
+            const int n = u * kGradThreads + tid, t = n & (kC - 1), vg = n / kC;
+            float e[8];
+            zero8(e);
+            if (8 * vg < a.dv) take8(reinterpret_cast<const float *>(smem) + (size_t)n * 8, e);
+            put_parts(ei + (t >> 3) * 128 + vg * 1024 + (t & 7) * 16, L::kE, e);
+        }
+        // [dR; dO] as left operand, half of the columns a thread
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int n = u * kGradThreads + tid, t = n & (kC - 1), vg = n / kC;
-                if (n < kC * DVT / 8) put_parts(ei + (t >> 3) * 128 + vg * 1024 + (t & 7) * 16, L::kE, f[u]);
+        for (int n = 0; n < KV / 2; ++n) {
+            const int ks = half * (KV / 2) + n;
+            float x[16];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int v = 16 * ks + 8 * m;
+                float y[8];
+                zero8(y);
+                if (low) {
+                    if (v < a.dv) take8(reinterpret_cast<const float *>(smem + kC * DVT * 4) + ((v >> 3) * kC + i) * 8, y);
+                } else {
+                    take8(reinterpret_cast<const T *>(smem + 2 * kC * DVT * 4 + i * L::kRow) + v, y);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[8 * m + j] = y[j];
             }
-            get_state<DKT, DVT>(f, 0, us, a.dk, a.dv, tid);
-            if constexpr (KV > 4) put_x(fx, 4);
+            tm_split16(mine + kTmA + 16 * ks, mine + kTmA + DVT + 8 * ks, x);
         }
         barrier();
         // S0 as right operand, columns dk, K = v, beside the first product
@@ -506,6 +510,7 @@ __global__ void __launch_bounds__(kGradBlock, 1)
         const float sr = low ? -eg[i] : a.scale * eg[i];
         if constexpr (L::kBeside) dot[half * 2 * kC + R] = sr * take(kTmD, sr);   // beside the product
         wait1();
+        if (L::kBeside && g + 1 < per) load_do(g + 1);
         if constexpr (!L::kBeside) {
             barrier();
             load_kq();

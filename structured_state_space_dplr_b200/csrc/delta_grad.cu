@@ -20,7 +20,12 @@
 // scalings of rows are scalings of threads. S0, dS1, E and dR are 192 KB in
 // float at Dk = Dv = 128, read once and split into bf16 parts here. (As parts,
 // stored by the chains and copied in bulk, they are half as much again, and
-// <S0, dS1> then costs the backward chain more than the copies save.)
+// <S0, dS1> then costs the backward chain more than the copies save.) That
+// space allows one block per SM; what bounds it is the chain of conversions and
+// products of a head. Measured: 4 x 4096 tokens, 16 key and 32
+// value heads of 128 bf16 (4096 blocks) 1021 us, 1.9 GB read a time; tensor
+// cores 27%, issue slots 28%. A head's E, dR and dO come to shared memory one
+// head ahead, 1094 us without.
 #include "delta.cuh"
 #include "s4dplr.h"
 

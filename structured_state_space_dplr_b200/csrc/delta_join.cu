@@ -7,7 +7,7 @@
 // thread one row of the result and 8 of the columns; M (by columns going
 // forward, by rows going back: the row index runs over the threads) comes into
 // shared memory one segment ahead. Read from L2 in the loop instead a segment
-// took 11 us.
+// took 11 us. Measured: 8 heads of 128 x 128 in 18 segments 37 us.
 #include "delta.cuh"
 #include "s4dplr.h"
 

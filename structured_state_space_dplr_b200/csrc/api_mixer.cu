@@ -82,13 +82,13 @@ struct DeltaWork {
     size_t state, rows, prep, sums, total;   // bytes of one kind
     int seg;
 };
-DeltaWork delta_work(int dtype, int Bt, long long tokens, int Hk, int Hv, int Dk, int Dv, int keep) {
+DeltaWork delta_work(int dtype, bool packed, int Bt, long long tokens, int Hk, int Hv, int Dk, int Dv, int keep) {
     DeltaWork w;
     const long long units = (tokens / 64 + Bt) * (long long)Hv;
     w.prep = s4::delta_prep_bytes(dtype, tokens, Bt, Hk, Hv, Dk);
     w.state = keep ? (size_t)units * Dk * Dv * 4 : 0;
     w.rows = keep ? (size_t)units * 64 * Dv * 4 : 0;
-    w.seg = s4::delta_segment(tokens, Bt, Hv);
+    w.seg = s4::delta_segment(tokens, Bt, Hv, packed);
     w.sums = s4::delta_segment_bytes(tokens, Bt, Hv, Dk, Dv, w.seg, keep);
     w.total = w.prep + 2 * w.state + 2 * w.rows + w.sums;
     return w;
@@ -200,7 +200,9 @@ s4_status s4_gated_delta_workspace_size(s4_dtype dtype, int Bt, long long tokens
     if (!bytes) return S4_ERR_INVALID_ARG;
     s4_status s = chunk_sizes(dtype, true, Bt, tokens, Hk, Hv, Dk, Dv);
     if (s != S4_OK) return s;
-    *bytes = delta_work(dtype, Bt, tokens, Hk, Hv, Dk, Dv, keep).total;
+    const size_t packed = delta_work(dtype, true, Bt, tokens, Hk, Hv, Dk, Dv, keep).total;
+    const size_t equal = delta_work(dtype, false, Bt, tokens, Hk, Hv, Dk, Dv, keep).total;
+    *bytes = packed > equal ? packed : equal;
     return S4_OK;
 }
 
@@ -216,7 +218,7 @@ s4_status s4_gated_delta_forward(s4_dtype dtype, const void *q, long long q_stri
     if (tokens > 0 && any_null({q, k, v, g, beta, o})) return S4_ERR_INVALID_ARG;
     if (!aligned(16, {q, k, v, o, initial_state, final_state}) || !aligned(4, {g, beta, cu_seqlens, d_flags}))
         return S4_ERR_INVALID_ARG;
-    const DeltaWork w = delta_work(dtype, Bt, tokens, Hk, Hv, Dk, Dv, keep);
+    const DeltaWork w = delta_work(dtype, cu_seqlens != nullptr, Bt, tokens, Hk, Hv, Dk, Dv, keep);
     if (!workspace || !aligned(256, {workspace}) || workspace_bytes < w.total) return S4_ERR_WORKSPACE;
     const double tok = (double)tokens, gate = tok * Hv * 4.0, st = 4.0 * Bt * Hv * Dk * Dv;
     // final_state may be initial_state: a state is read before it is written
@@ -258,7 +260,7 @@ s4_status s4_gated_delta_backward(s4_dtype dtype, const float *g, const float *b
     if (!aligned(16, {d_o, dq, dk, dv, d_final_state, d_initial_state}) ||
         !aligned(4, {g, beta, dg, dbeta, cu_seqlens, d_flags}))
         return S4_ERR_INVALID_ARG;
-    const DeltaWork w = delta_work(dtype, Bt, tokens, Hk, Hv, Dk, Dv, 1);
+    const DeltaWork w = delta_work(dtype, cu_seqlens != nullptr, Bt, tokens, Hk, Hv, Dk, Dv, 1);
     if (!workspace || !aligned(256, {workspace}) || workspace_bytes < w.total) return S4_ERR_WORKSPACE;
     const double tok = (double)tokens, gate = tok * Hv * 4.0, st = 4.0 * Bt * Hv * Dk * Dv;
     const double nk = tok * Hk * Dk * dtype_size(dtype), nv = tok * Hv * Dv * dtype_size(dtype);

@@ -423,12 +423,18 @@ cudaError_t run(const DeltaArgs &a, const float *init, float *last, const void *
 // what each does to the state is computed for all at once (twice the chain's
 // work: M and N), joined, and the segments run again from their states. Times
 // in chunks of a chain (3.1 us; M and N without output 0.85 of that, a join
-// 0.8, the extra launches 4), for sequences of average length. One sequence of
+// 0.8, the extra launches 4). Lengths of packed sequences are not known here;
+// the longest is taken as it is on average when `tokens` are cut at random
+// places, H_n / n of them (H_n the harmonic number): 8192 tokens in sequences
+// of 4000, 500, 1000, 692 and four of 500, 8 heads, 314 us in one piece each
+// and 138 in segments; where all have 1024, 88 and 126. One sequence of
 // 65536 tokens, 8 heads of 128: 3515 us for the whole call in one piece, 911
 // us in 18.
-int delta_segment(long long tokens, int n, int hv) {
+int delta_segment(long long tokens, int n, int hv, bool packed) {
     constexpr double kSms = 148;
-    const double chains = (double)n * hv, c = ceil((double)tokens / kC / n);
+    const double all = (double)tokens / kC, cuts = packed && n > 1 ? log((double)n) + 0.577 + 0.5 / n : 1;
+    // the longest sequence, and how many as long make up all tokens
+    const double c = ceil(all / n * cuts), chains = n / cuts * hv;
     double best = 0.9 * ceil(chains / kSms) * c;
     int seg = 0;
     for (int k = 3; k <= 64 && k <= c; ++k) {

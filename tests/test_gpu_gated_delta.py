@@ -180,6 +180,13 @@ def test_packed(cu, dtype, shape):
             assert torch.equal(final[i], d["state"][i]) and torch.equal(got["initial_state"][i], ds[i])
 
 
+# most tokens in one of several sequences, which then run in segments of their own number
+@pytest.mark.parametrize("cu", [[0, 2500, 2500, 2501, 2740], [0, 200, 500, 2730, 2731], [7, 900, 1700, 2600, 2731]])
+@pytest.mark.parametrize("dtype,shape", [("float16", (1, 3, 96, 80)), ("float32", (2, 2, 64, 128))])
+def test_packed_of_unequal_lengths(cu, dtype, shape):
+    test_packed(cu, dtype, shape)
+
+
 @pytest.mark.parametrize("shape", [(1, 1500, 1, 2, 64, 64), (1, 3000, 2, 2, 128, 96), (2, 2000, 1, 1, 40, 128)])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_few_long_sequences_run_in_segments(shape, dtype):

@@ -7,7 +7,7 @@
 //
 // Both directions move each array once (rows: forward x -> z, backward x, dz
 // -> dx; channels: x, dz -> dx). Measured at 32768 rows of 1024 bf16: forward
-// 41 us (3.2 TB/s), backward 51 + 5.5 us (3.6 TB/s), both nearer to the issue
+// 39 us (3.4 TB/s), backward 50 + 5.5 us (3.6 TB/s), both nearer to the issue
 // rate of their conversions and sums than to memory; 16384 rows of 2048 float,
 // backward: 67 us (6.0 TB/s). Channels, 8 x 256 x 16384: 81 us (4.9 TB/s). The weight gradients are summed in
 // registers over all rows a block visits (a fixed set, in a fixed order),
@@ -104,24 +104,23 @@ struct Weights {
     }
 };
 
-// Rows of 16- or 8-byte packs go through a ring in shared memory: kStages - 1 rounds
-// of rows are on their way while one is reduced, two rows a round where a row
-// takes one pack a thread. A thread copies exactly what it reads, so the ring
-// needs no barrier, and it reads a pack again rather than keep it: with the rows
-// in registers the loads in flight were paid for in occupancy (32768 rows of
-// 1024 bf16: forward 86 us a row a block, 49 us four rows at a time, 41 us now;
-// backward 74, 117 and 51 us; float rows reach 4.5 and 6.0 TB/s, bf16 ones are
-// bound by their instructions). 8-byte packs: rows that are multiples of 8 bytes
-// only (30000 of 500 bf16, backward: 36 us, as single elements 63). Single
-// elements (V = 1) are loaded where they are used.
+// Rows of 16- or 8-byte packs go through a ring in shared memory: kStages - 1
+// rounds of rows are on their way while one is reduced, two rows a round where
+// a row takes few packs a thread. A thread copies exactly what it reads, so the
+// ring needs no barrier. With the loads in flight in registers they were paid
+// for in occupancy (32768 rows of 1024 bf16: forward 86 us a row a block, 49 us
+// four rows at a time, 39 us now; backward 74, 117 and 50 us; float rows reach
+// 5.2 and 6.0 TB/s, bf16 ones are bound by their instructions). 8-byte packs:
+// rows that are multiples of 8 bytes only (30000 of 500 bf16, backward: 30 us,
+// as single elements 63). Single elements (V = 1) are loaded where they are used.
 constexpr int kStages = 3;
-template <int V, int NV>
-__host__ __device__ constexpr int rows_at_once() { return V > 1 && NV <= 2 ? 2 : 1; }
+template <int V, int NV, int ARR>
+__host__ __device__ constexpr int rows_at_once() { return V > 1 && NV * ARR <= 2 ? 2 : 1; }
 
 // ARR arrays of rows; ring [stage][row][array][NV][thread]
 template <typename T, int V, int NV, int ARR>
 struct Rows {
-    static constexpr int R = rows_at_once<V, NV>();
+    static constexpr int R = rows_at_once<V, NV, ARR>();
     Pack<T, V> *ring;
     const T *src[ARR];
     long long rows;
@@ -198,57 +197,60 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_rows(const T *x, const float
     for (long long r0 = first; r0 < rows; r0 += stride, in.step()) {
         const long long r = r0 + mine;
         in.ahead(r, stride);
-        float s[R], mu[R];
+        float s[R], mu[R], v[R][NV][V];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             s[q] = 0.0f;
-            if (r + q < rows)
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if ((l + i * tpr) * V < D) {
-                        float v[V];
-                        in.get(r, q, 0, i, v);
+            for (int i = 0; i < NV; ++i) {
+                if (r + q < rows && (l + i * tpr) * V < D)
+                    in.get(r, q, 0, i, v[q][i]);
+                else
 #pragma unroll
-                        for (int j = 0; j < V; ++j) s[q] += v[j];
-                    }
+                    for (int j = 0; j < V; ++j) v[q][i][j] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[q] += v[q][i][j];
+            }
         }
         group_sum<R, BIG>(s, tpr, buf, turn);
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             mu[q] = s[q] * inv;
             s[q] = 0.0f;
-            if (r + q < rows)
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if ((l + i * tpr) * V < D) {
-                        float v[V];
-                        in.get(r, q, 0, i, v);
+            for (int i = 0; i < NV; ++i)
+                if ((l + i * tpr) * V < D)
 #pragma unroll
-                        for (int j = 0; j < V; ++j) s[q] = fmaf(v[j] - mu[q], v[j] - mu[q], s[q]);
+                    for (int j = 0; j < V; ++j) {
+                        v[q][i][j] -= mu[q];
+                        s[q] = fmaf(v[q][i][j], v[q][i][j], s[q]);
                     }
         }
         group_sum<R, BIG>(s, tpr, buf, turn);
+        float rs[R];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            if (r + q >= rows) continue;
-            const float rs = 1.0f / sqrtf(fmaf(s[q], inv, eps));
-            if (l == 0) {
+            rs[q] = 1.0f / sqrtf(fmaf(s[q], inv, eps));
+            if (l == 0 && r + q < rows) {
                 mean[r + q] = mu[q];
-                rstd[r + q] = rs;
+                rstd[r + q] = rs[q];
             }
+        }
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (l + i * tpr) * V;
-                if (c < D) {
-                    float o[V], g[V], b[V];
-                    ga.get(i, g);
-                    be.get(i, b);
-                    in.get(r, q, 0, i, o);
+        for (int i = 0; i < NV; ++i) {
+            const int c = (l + i * tpr) * V;
+            if (c >= D) continue;
+            float g[V], b[V];
+            ga.get(i, g);
+            be.get(i, b);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) o[j] = fmaf((o[j] - mu[q]) * rs, g[j], b[j]);
+            for (int q = 0; q < R; ++q)
+                if (r + q < rows) {
+                    float o[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) o[j] = fmaf(v[q][i][j] * rs[q], g[j], b[j]);
                     store_pack<T, V>(z + (r + q) * D + c, o);
                 }
-            }
         }
     }
 }
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_rows_backward(
     for (long long r0 = first; r0 < rows; r0 += stride, in.step()) {
         const long long r = r0 + mine;
         in.ahead(r, stride);
-        float s[2 * R], mu[R], rs[R];
+        float s[2 * R], mu[R], rs[R], xh[R][NV][V], h[R][NV][V];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             s[2 * q] = s[2 * q + 1] = 0.0f;
@@ -297,17 +299,19 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_rows_backward(
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     if ((l + i * tpr) * V < D) {
-                        float v[V], d[V], g[V];
+                        float g[V];
                         ga.get(i, g);
-                        in.get(r, q, 0, i, v);
-                        in.get(r, q, 1, i, d);
+                        in.get(r, q, 0, i, xh[q][i]);
+                        in.get(r, q, 1, i, h[q][i]);
 #pragma unroll
                         for (int j = 0; j < V; ++j) {
-                            const float xh = (v[j] - mu[q]) * rs[q], h = d[j] * g[j];
-                            dg[i][j] = fmaf(d[j], xh, dg[i][j]);
-                            db[i][j] += d[j];
-                            s[2 * q] += h;
-                            s[2 * q + 1] = fmaf(h, xh, s[2 * q + 1]);
+                            const float d = h[q][i][j], x = (xh[q][i][j] - mu[q]) * rs[q];
+                            dg[i][j] = fmaf(d, x, dg[i][j]);
+                            db[i][j] += d;
+                            xh[q][i][j] = x;
+                            h[q][i][j] = d * g[j];
+                            s[2 * q] += h[q][i][j];
+                            s[2 * q + 1] = fmaf(h[q][i][j], x, s[2 * q + 1]);
                         }
                     }
         }
@@ -321,13 +325,20 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_rows_backward(
             for (int i = 0; i < NV; ++i) {
                 const int c = (l + i * tpr) * V;
                 if (c < D) {
-                    float o[V], d[V], g[V];
-                    ga.get(i, g);
-                    in.get(r, q, 0, i, o);
-                    in.get(r, q, 1, i, d);
+                    if constexpr (sizeof(T) == 4) {   // read again: nothing to convert, and registers are short
+                        float g[V];
+                        ga.get(i, g);
+                        in.get(r, q, 0, i, xh[q][i]);
+                        in.get(r, q, 1, i, h[q][i]);
 #pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        o[j] = rs[q] * (d[j] * g[j] - fmaf((o[j] - mu[q]) * rs[q], m1, m0));
+                        for (int j = 0; j < V; ++j) {
+                            xh[q][i][j] = (xh[q][i][j] - mu[q]) * rs[q];
+                            h[q][i][j] *= g[j];
+                        }
+                    }
+                    float o[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) o[j] = rs[q] * (h[q][i][j] - fmaf(xh[q][i][j], m1, m0));
                     store_pack<T, V>(dx + (r + q) * D + c, o);
                 }
             }
@@ -628,11 +639,11 @@ __global__ void __launch_bounds__(256) k_layernorm_channels_backward(
 }
 
 // How a row of D elements is spread: V per access, NV accesses by each of tpr
-// threads, at most kForward or kBackward elements a thread (8 when single). As
-// few threads as that allows: a row's reductions and addresses cost every warp
-// of it the same. The backward pass keeps two sums an element, and at 32 of
-// them a thread too few warps fit (32768 rows of 1024 bf16: 97 us).
-constexpr int kForward = 32, kBackward = 16;
+// threads, at most kElements elements a thread (8 when single). Fewer threads
+// make a row's reductions and addresses cost fewer warps; 32 elements a thread
+// leave too few warps for their registers (16384 rows of 2048, forward: 41 us
+// bf16 and 64 us float, 38 and 52 with 16; backward at 32, 1024 bf16: 97 us).
+constexpr int kElements = 16;
 struct RowPlan { int v, nv, tpr, block; };
 
 RowPlan row_plan(int D, int elem, int bytes, int elements) {
@@ -730,11 +741,11 @@ size_t norm_backward_workspace_bytes(int D) { return (size_t)most_blocks(D) * 2 
 cudaError_t launch_layernorm_rows(int dtype, const void *x, const float *gamma, const float *beta, float eps,
                                   long long rows, int D, void *z, float *mean, float *rstd, cudaStream_t st) {
     if (rows == 0) return cudaSuccess;
-    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, access_bytes(dtype, D, x, z, nullptr), kForward);
+    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, access_bytes(dtype, D, x, z, nullptr), kElements);
     cudaError_t err = cudaSuccess;
     with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        with_plan<T, kForward>(p, [&](auto v, auto nv, auto big, auto most) {
+        with_plan<T, kElements>(p, [&](auto v, auto nv, auto big, auto most) {
             constexpr int V = decltype(v)::value, NV = decltype(nv)::value, MAXT = decltype(most)::value;
             static Resident resident;
             static SmemLimit limit;
@@ -742,7 +753,7 @@ cudaError_t launch_layernorm_rows(int dtype, const void *x, const float *gamma, 
             const size_t smem = Rows<T, V, NV, 1>::bytes(p.block);
             err = limit.raise(kernel, smem);
             if (err != cudaSuccess) return;
-            const int grid = row_blocks(rows, p, rows_at_once<V, NV>(), 148 * resident.of(kernel, p.block, smem));
+            const int grid = row_blocks(rows, p, rows_at_once<V, NV, 1>(), 148 * resident.of(kernel, p.block, smem));
             kernel<<<grid, p.block, smem, st>>>((const T *)x, gamma, beta, eps, rows, D, p.tpr, (T *)z, mean, rstd);
         });
     });
@@ -752,7 +763,7 @@ cudaError_t launch_layernorm_rows(int dtype, const void *x, const float *gamma, 
 cudaError_t launch_layernorm_rows_backward(int dtype, const void *dz, const void *x, const float *gamma,
                                            const float *mean, const float *rstd, long long rows, int D, void *dx,
                                            float *dgamma, float *dbeta, void *ws, cudaStream_t st) {
-    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, access_bytes(dtype, D, x, dz, dx), kBackward);
+    const RowPlan p = row_plan(D, dtype == S4_F32 ? 4 : 2, access_bytes(dtype, D, x, dz, dx), kElements);
     int grid = 0;
     // several groups in a block only for tpr <= 32: D <= 1024
     const size_t acc = p.block > p.tpr ? (size_t)2 * D * sizeof(float) : 0;
@@ -760,7 +771,7 @@ cudaError_t launch_layernorm_rows_backward(int dtype, const void *dz, const void
     float *part = (float *)ws;
     if (rows > 0) with_type(dtype, [&](auto t) {   // no rows: zero gradients from no partial rows
         using T = decltype(t);
-        with_plan<T, kBackward>(p, [&](auto v, auto nv, auto big, auto most) {
+        with_plan<T, kElements>(p, [&](auto v, auto nv, auto big, auto most) {
             constexpr int V = decltype(v)::value, NV = decltype(nv)::value, MAXT = decltype(most)::value;
             static Resident resident;
             static SmemLimit limit;
@@ -769,7 +780,7 @@ cudaError_t launch_layernorm_rows_backward(int dtype, const void *dz, const void
             err = limit.raise(kernel, smem);
             if (err != cudaSuccess) return;
             const int fit = 148 * resident.of(kernel, p.block, smem);
-            grid = row_blocks(rows, p, rows_at_once<V, NV>(), fit < most_blocks(D) ? fit : most_blocks(D));
+            grid = row_blocks(rows, p, rows_at_once<V, NV, 2>(), fit < most_blocks(D) ? fit : most_blocks(D));
             kernel<<<grid, p.block, smem, st>>>(
                 (const T *)dz, (const T *)x, gamma, mean, rstd, rows, D, p.tpr, (T *)dx, part);
         });

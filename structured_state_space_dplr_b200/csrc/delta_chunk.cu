@@ -428,7 +428,7 @@ cudaError_t run(const DeltaArgs &a, const float *init, float *last, const void *
 // places, H_n / n of them (H_n the harmonic number): 8192 tokens in sequences
 // of 4000, 500, 1000, 692 and four of 500, 8 heads, 314 us in one piece each
 // and 138 in segments; where all have 1024, 88 and 126. One sequence of
-// 65536 tokens, 8 heads of 128: 3515 us for the whole call in one piece, 911
+// 65536 tokens, 8 heads of 128: 3515 us for the whole call in one piece, 907
 // us in 18.
 int delta_segment(long long tokens, int n, int hv, bool packed) {
     constexpr double kSms = 148;

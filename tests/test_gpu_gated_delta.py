@@ -296,6 +296,50 @@ def test_strided_tokens_and_streams_and_graph():
     assert torch.equal(o, want[0]) and torch.equal(last, want[1]) and all(torch.equal(g3[m], grads[m]) for m in grads)
 
 
+def test_segments_in_a_graph_and_two_calls_at_once():
+    """A captured call in segments answers for the inputs and offsets of its
+    replay, not of its capture; a workspace is used again; calls on two
+    streams with workspaces of their own do not touch each other."""
+    torch = torch_cuda()
+    import structured_state_space_dplr_b200 as s4
+    d = make(1, 2740, 1, 3, 64, 64, "bfloat16")
+    other = make(1, 2740, 1, 3, 64, 64, "bfloat16", seed=9)
+    do = torch.randn(d["v"].shape, device="cuda", generator=gen(1)).to(torch.bfloat16)
+    cu = torch.tensor([0, 2500, 2501, 2740], dtype=torch.int32, device="cuda")
+    cu2 = torch.tensor([3, 200, 400, 2739], dtype=torch.int32, device="cuda")
+    run = lambda x, c, w=None: (  # noqa: E731
+        lambda f: (f[0], f[1], *s4.gated_delta_backward(*(x[n] for n in NAMES), do, f[2], cu_seqlens=c).values()))(
+            s4.gated_delta_forward(*(x[n] for n in NAMES), cu_seqlens=c, keep=True, workspace=w,
+                                   out=torch.zeros_like(x["v"])))
+    first, second = run(d, cu), run(other, cu2)
+    work = torch.empty(s4.gated_delta_workspace_size(torch.bfloat16, 3, 2740, 1, 3, 64, 64, True), dtype=torch.uint8,
+                       device="cuda").fill_(255)
+    x, c = {n: d[n].clone() for n in NAMES}, cu.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(x, c, work)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, first))
+    for n in NAMES:
+        x[n].copy_(other[n])
+    c.copy_(cu2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, second))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    results = [[], []]
+    for i, (y, k) in enumerate(((d, cu), (other, cu2))):
+        streams[i].wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for i, (y, k) in enumerate(((d, cu), (other, cu2))):
+            with torch.cuda.stream(streams[i]):
+                results[i].append(run(y, k))
+    torch.cuda.synchronize()
+    for got, want in zip(results, (first, second)):
+        assert all(torch.equal(a, b) for r in got for a, b in zip(r, want))
+
+
 def test_refusals():
     torch = torch_cuda()
     import structured_state_space_dplr_b200 as s4

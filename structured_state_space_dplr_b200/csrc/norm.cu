@@ -819,7 +819,7 @@ cudaError_t launch_layernorm_channels_backward(const float *dz, const float *x, 
         if (e != cudaSuccess) return e;
     } else {
         const int smem = 2 * H * (int)sizeof(float);
-        if (smem > 48 * 1024) {
+        if (smem > 40 * 1024) {   // with the static 4 KB above the 48 KB that need no asking
             cudaError_t e = cudaFuncSetAttribute(k_layernorm_channels_backward,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  2 * S4_MAX_BLOCK_H * (int)sizeof(float));

@@ -131,6 +131,20 @@ def test_channels(Bt, H, L):
     assert all(torch.equal(a, b) for a, b in zip((dx, dg, db), again))
 
 
+def test_channels_of_every_width_in_a_new_process():
+    """From 5633 channels on the weight gradients and the kernel's static
+    shared memory together pass the 48 KB that a launch has unasked; in a
+    process of its own, where no wider call has raised the limit before."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import sys; sys.path[:0] = [%r, %r]; import test_gpu_norm as t\n"
+            "for H in (5632, 5633, 5640, 6144, 6145): t.test_channels(1, H, 16)" % (os.path.dirname(here), here))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_channels_backward_fits_its_forward():
     """The directional difference of s4.layernorm_channels itself."""
     torch = torch_cuda()

@@ -1,21 +1,31 @@
 // launch.h -- internal host-side launchers (one per kernel family).
 #pragma once
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
+#include <mutex>
 
 namespace s4 {
 
-// A kernel's limit of dynamic shared memory, raised once per device (raising it
-// twice, from two threads, is harmless).
+// A kernel's limit of dynamic shared memory per device, raised to the largest
+// size asked for and never lowered: calls of different sizes share a kernel and
+// may come from several host threads at once, so that the limit and the record
+// of it change together, under the lock.
 struct SmemLimit {
-    size_t set[64] = {};
+    static constexpr int kDevices = 64;
+    std::atomic<size_t> set[kDevices] = {};
+    std::mutex change;
     template <typename K>
     cudaError_t raise(K *kernel, size_t bytes) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess || (dev < 64 && set[dev] >= bytes)) return e;
+        if (e != cudaSuccess) return e;
+        if (dev >= kDevices) return cudaErrorInvalidDevice;
+        if (set[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+        std::lock_guard<std::mutex> lock(change);
+        if (set[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        if (e == cudaSuccess && dev < 64) set[dev] = bytes;
+        if (e == cudaSuccess) set[dev].store(bytes, std::memory_order_release);
         return e;
     }
 };

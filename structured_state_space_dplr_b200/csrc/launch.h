@@ -30,6 +30,23 @@ struct SmemLimit {
     }
 };
 
+// Blocks of a kernel that an SM holds, asked for once per block size, which
+// sets the shared memory (the same on every device this library runs on).
+// Threads that ask at the same time write the same number.
+struct Resident {
+    std::atomic<int> n[33] = {};   // by block size / 32
+    template <typename K>
+    int of(K *kernel, int block, size_t smem) {
+        std::atomic<int> &r = n[block / 32];
+        int b = r.load(std::memory_order_relaxed);
+        if (b == 0) {
+            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, block, smem) != cudaSuccess || b < 1) b = 1;
+            r.store(b, std::memory_order_relaxed);
+        }
+        return b;
+    }
+};
+
 // remember a failing CUDA call for s4_last_cuda_error() (calling host thread)
 void record_cuda_error(cudaError_t e);
 

@@ -700,22 +700,6 @@ void with_plan(const RowPlan &p, F &&f) {
         go(integral_constant<int, VV>{}, integral_constant<int, ELEMENTS / VV>{});
 }
 
-// blocks of a kernel that an SM holds, asked for once per block size, which
-// sets the shared memory (the same on every device this library runs on)
-struct Resident {
-    int n[33] = {};   // by block size / 32
-    template <typename K>
-    int of(K *kernel, int block, size_t smem) {
-        int &r = n[block / 32];
-        if (r == 0) {
-            int b = 0;
-            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, block, smem) != cudaSuccess || b < 1) b = 1;
-            r = b;
-        }
-        return r;
-    }
-};
-
 template <typename F>
 void with_type(int dtype, F &&f) {
     if (dtype == S4_BF16)

@@ -24,3 +24,7 @@ def run(tmp_path, source, *flags):
 @pytest.mark.parametrize("flags", [(), ("-fsanitize=thread",)])
 def test_shared_memory_limit_from_two_threads(tmp_path, flags):
     run(tmp_path, "smem_limit.cpp", *flags)
+
+
+def test_resident_blocks_from_four_threads(tmp_path):
+    run(tmp_path, "resident.cpp", "-fsanitize=thread")

@@ -658,7 +658,9 @@ s4_status s4_gated_delta_scan(s4_dtype dtype, const void *q, long long q_stride,
  *   keep != 0 leaves in the workspace what s4_gated_delta_backward reads
  *     (states before the chunks and the chunks' writes).
  *   workspace: s4_gated_delta_workspace_size(...) bytes for the
- *     same sizes, device, 256-byte aligned, caller-owned.
+ *     same sizes, device, 256-byte aligned, caller-owned. One for more tokens
+ *     (of as many sequences and heads) is large enough for fewer; fewer
+ *     sequences may need more, where they run in segments.
  *   d_flags (nullable): S4_FLAG_TIMEOUT if a bounded wait ran out.
  * Operands that are not bf16 are split into bf16 parts (three for float: 24
  * bits) and accumulated in float: results are as good as float arithmetic's.

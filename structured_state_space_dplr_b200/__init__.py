@@ -802,7 +802,7 @@ def gated_delta_step(q, k, v, g, beta, state, *, scale=None, out=None):
 def gated_delta_workspace_size(dtype, Bt, tokens, Hk, Hv, Dk, Dv, keep=False) -> int:
     """Bytes of workspace gated_delta_forward needs for `tokens` tokens in all
     of Bt sequences of the torch dtype (keep: and for gated_delta_backward
-    after it)."""
+    after it). Enough for fewer tokens too, not always for fewer sequences."""
     if dtype not in _DTYPES:
         raise TypeError("float32, bfloat16 or float16 is wanted")
     n = ctypes.c_size_t(0)

@@ -88,8 +88,9 @@ DeltaWork delta_work(int dtype, bool packed, int Bt, long long tokens, int Hk, i
     w.prep = s4::delta_prep_bytes(dtype, tokens, Bt, Hk, Hv, Dk);
     w.state = keep ? (size_t)units * Dk * Dv * 4 : 0;
     w.rows = keep ? (size_t)units * 64 * Dv * 4 : 0;
-    w.seg = s4::delta_segment(tokens, Bt, Hv, packed);
-    w.sums = s4::delta_segment_bytes(tokens, Bt, Hv, Dk, Dv, w.seg, keep);
+    long long segments;
+    w.seg = s4::delta_segment(tokens, Bt, Hv, packed, &segments);
+    w.sums = s4::delta_segment_bytes(segments, Hv, Dk, Dv, keep);
     w.total = w.prep + 2 * w.state + 2 * w.rows + w.sums;
     return w;
 }

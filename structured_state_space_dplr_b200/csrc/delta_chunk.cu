@@ -430,26 +430,48 @@ cudaError_t run(const DeltaArgs &a, const float *init, float *last, const void *
 // and 138 in segments; where all have 1024, 88 and 126. One sequence of
 // 65536 tokens, 8 heads of 128: 3515 us for the whole call in one piece, 907
 // us in 18.
-int delta_segment(long long tokens, int n, int hv, bool packed) {
+//
+// A workspace for many tokens has to serve calls with fewer. The best number of
+// segments goes up and down with the length where they are a few chunks each
+// and the last is not full. Without that rounding a number's time is a line in
+// the length, steeper and from a lower start the fewer they are, so the best
+// one only rises with the length. Up to a quarter more than that may be taken
+// (the rule finds its best among them in 99 of 100 lengths, and within 4% in
+// the others), and room is kept for as many: at most n most / cuts + 2 n.
+int delta_segment(long long tokens, int n, int hv, bool packed, long long *count) {
     constexpr double kSms = 148;
+    constexpr int kMost = 64;
     const double all = (double)tokens / kC, cuts = packed && n > 1 ? log((double)n) + 0.577 + 0.5 / n : 1;
     // the longest sequence, and how many as long make up all tokens
-    const double c = ceil(all / n * cuts), chains = n / cuts * hv;
-    double best = 0.9 * ceil(chains / kSms) * c;
+    const double c = ceil(all / n * cuts), chains = n / cuts * hv, one = 0.9 * ceil(chains / kSms) * c;
+    double per[kMost + 1], best = one;   // per: time by chunks of a segment
+    int unrounded = 0;
+    for (int k = 3; k <= kMost && k <= c; ++k) {
+        per[k] = 0.85 * ceil(2 * chains * (k - 1) / kSms) + ceil(chains * k / kSms);
+        const double t = per[k] * c / k + 0.8 * k + 4;
+        if (t < best) {
+            best = t;
+            unrounded = k;
+        }
+    }
+    const int most = (5 * unrounded + 3) / 4;
     int seg = 0;
-    for (int k = 3; k <= 64 && k <= c; ++k) {
-        const double len = ceil(c / k), t = ceil(2 * chains * (k - 1) / kSms) * len * 0.85 +
-                                            ceil(chains * k / kSms) * len + 0.8 * k + 4;
+    best = one;
+    for (int k = 3; k <= most && k <= kMost && k <= c; ++k) {
+        const double len = ceil(c / k), t = per[k] * len + 0.8 * k + 4;
         if (t < best) {
             best = t;
             seg = (int)len;
         }
     }
+    *count = most ? (long long)ceil(n * most / cuts) + 2 * (long long)n : 0;
+    const long long used = seg ? segments(slots(tokens, n), n, seg) : 0;
+    if (*count < used) *count = used;
     return seg;
 }
 
-size_t delta_segment_bytes(long long tokens, int n, int hv, int dk, int dv, int seg, bool keep) {
-    return seg ? (size_t)segments(slots(tokens, n), n, seg) * hv * Summaries(dk, dv, keep).unit() * sizeof(float) : 0;
+size_t delta_segment_bytes(long long count, int hv, int dk, int dv, bool keep) {
+    return (size_t)count * hv * Summaries(dk, dv, keep).unit() * sizeof(float);
 }
 
 cudaError_t launch_delta_forward(int dtype, const DeltaArgs &a, const float *init, float *last, const void *ws,

@@ -160,9 +160,9 @@ cudaError_t launch_delta_prep(int dtype, const DeltaArgs &a, void *ws, unsigned 
 // a.seg > 0: each sequence in segments, summaries: delta_segment_bytes of scratch
 cudaError_t launch_delta_forward(int dtype, const DeltaArgs &a, const float *init, float *last, const void *ws,
                                  float *keep_s, float *keep_e, void *summaries, unsigned *flags, cudaStream_t st);
-// whether splitting pays: chunks of a segment, or 0
-int delta_segment(long long tokens, int n, int hv, bool packed);
-size_t delta_segment_bytes(long long tokens, int n, int hv, int dk, int dv, int seg, bool keep);
+// whether splitting pays: chunks of a segment, or 0; *count: segments to keep room for, never fewer for more tokens
+int delta_segment(long long tokens, int n, int hv, bool packed, long long *count);
+size_t delta_segment_bytes(long long count, int hv, int dk, int dv, bool keep);
 // the states before the segments from init; back: the states' gradients behind them from init
 cudaError_t launch_delta_join(const DeltaArgs &a, const float *init, float *sums, bool keep, bool back, unsigned *flags,
                               cudaStream_t st);

@@ -92,3 +92,16 @@ def test_gated_delta_chunks_reject_bad_arguments(lib):
     assert b(do=p(0)) == b(dq=p(0)) == b(dg=p(0)) == b(tok=201) == b(Bt=0) == bad
     assert b(dv=do) == b(dq=dk) == b(dg=db) == b(dv=ws) == bad
     assert b(ws=p(0)) == b(nb=small) == _lib.S4_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("Bt,Hk,Hv,Dk,Dv", [(1, 4, 8, 128, 128), (1, 1, 1, 64, 64), (1, 1, 2, 8, 128), (2, 2, 4, 128, 96),
+                                            (4, 4, 8, 128, 128), (3, 1, 3, 72, 40), (8, 8, 16, 128, 128),
+                                            (13, 8, 16, 128, 128), (5, 2, 6, 96, 80), (1, 32, 32, 128, 128)])
+@pytest.mark.parametrize("keep", [0, 1])
+def test_gated_delta_workspace_for_more_tokens_serves_fewer(lib, Bt, Hk, Hv, Dk, Dv, keep):
+    n = ctypes.c_size_t()
+    last = 0
+    for tokens in [*range(0, 3000, 7), *range(3000, 80000, 64), *range(80000, 1000000, 640)]:
+        assert lib.s4_gated_delta_workspace_size(1, Bt, tokens, Hk, Hv, Dk, Dv, keep, ctypes.byref(n)) == 0
+        assert n.value >= last, tokens
+        last = n.value

@@ -384,3 +384,23 @@ def test_few_long_sequences_backward(shape, dtype):
         got = backward(d, do, work, scale=0.3, dfinal_state=ds)
         for m in (*NAMES, "initial_state"):      # one more chain and the joins, both ways
             check(got[m], ref[m], got[m].dtype, "d" + m, 4)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_one_workspace_for_all_lengths(packed):
+    """A workspace made for the longest call serves shorter ones, in segments
+    or not, whatever it holds."""
+    torch = torch_cuda()
+    import structured_state_space_dplr_b200 as s4
+    most, Hk, Hv, Dk, Dv = 3300, 1, 2, 64, 48
+    work = torch.empty(s4.gated_delta_workspace_size(torch.bfloat16, 2, most, Hk, Hv, Dk, Dv, True), dtype=torch.uint8,
+                       device="cuda")
+    for tokens in (2, 130, 1024, 1026, 1980, 2048, 2050, 3200, 3264, 3300):
+        d = make(1, tokens, Hk, Hv, Dk, Dv, "bfloat16") if packed else make(2, tokens // 2, Hk, Hv, Dk, Dv, "bfloat16")
+        cu = torch.tensor([0, tokens // 5, tokens], dtype=torch.int32, device="cuda") if packed else None
+        do = torch.randn(d["v"].shape, device="cuda", generator=gen(1)).to(torch.bfloat16)
+        results = []
+        for w in (None, work.fill_(255)):
+            o, last, kept = forward(d, cu_seqlens=cu, keep=True, workspace=w)
+            results.append((o, last, *backward(d, do, kept, cu_seqlens=cu).values()))
+        assert all(torch.equal(a, b) for a, b in zip(*results)), tokens

@@ -404,3 +404,54 @@ def test_one_workspace_for_all_lengths(packed):
             o, last, kept = forward(d, cu_seqlens=cu, keep=True, workspace=w)
             results.append((o, last, *backward(d, do, kept, cu_seqlens=cu).values()))
         assert all(torch.equal(a, b) for a, b in zip(*results)), tokens
+
+
+def used(d, n):
+    """A workspace of d's sizes for n sequences that holds what no call left: NaN in every type."""
+    torch = torch_cuda()
+    import structured_state_space_dplr_b200 as s4
+    (B, T, Hk, Dk), (Hv, Dv) = d["q"].shape, d["v"].shape[2:]
+    return torch.empty(s4.gated_delta_workspace_size(d["v"].dtype, n, B * T, Hk, Hv, Dk, Dv, True), dtype=torch.uint8,
+                       device="cuda").fill_(255)
+
+
+# In segments from no state: the first segment's M is not computed and the join
+# leaves its product out; backward, no gradient comes from behind the last one.
+@pytest.mark.parametrize("shape", [(1, 1500, 1, 2, 64, 64), (1, 2200, 2, 2, 128, 96), (2, 2000, 1, 1, 40, 128)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("state,dstate", [(False, False), (True, False), (False, True)])
+def test_segments_without_states(shape, dtype, state, dstate):
+    torch = torch_cuda()
+    d = make(*shape, dtype=dtype)
+    d["g"] *= 0.02
+    do = torch.randn(d["v"].shape, device="cuda", generator=gen(1)).to(d["v"].dtype)
+    ds = torch.randn(d["state"].shape, device="cuda", generator=gen(2)) if dstate else None
+    start = d["state"] if state else None
+    ref, last, gr = delta.gated_delta(*(f64(d[n]) for n in NAMES), 0.3, f64(start) if state else None, do=f64(do),
+                                      dstate=f64(ds) if dstate else None)
+    for keep in (False, True):
+        o, got, work = forward(d, scale=0.3, initial_state=start, keep=keep, workspace=used(d, shape[0]))
+        check(o, ref, d["v"].dtype, "o", 2)
+        check(got, last, torch.float32, "state", 2)
+    got = backward(d, do, work, scale=0.3, dfinal_state=ds)
+    for m in (*NAMES, "initial_state"):
+        check(got[m], gr[m], got[m].dtype, "d" + m, 4)
+
+
+@pytest.mark.parametrize("cu", [[0, 2500, 2500, 2501, 2740], [7, 900, 1700, 2600, 2731]])
+@pytest.mark.parametrize("dtype,shape", [("float16", (1, 3, 96, 80)), ("float32", (2, 2, 64, 128))])
+def test_packed_segments_without_states(cu, dtype, shape):
+    torch = torch_cuda()
+    T = cu[-1] + 9
+    d = make(1, T, *shape, dtype=dtype)
+    args = packed(d, cu)
+    do = torch.randn(d["v"].shape, device="cuda", generator=gen(1)).to(d["v"].dtype)
+    ref, last, gr = delta.gated_delta(*args, 0.5, None, cu=cu, do=f64(do))
+    o, final, work = forward(d, scale=0.5, cu_seqlens=d["cu"], keep=True, workspace=used(d, len(cu) - 1))
+    check(o, ref, o.dtype, "o")
+    check(final, last, torch.float32, "state")
+    got = backward(d, do, work, scale=0.5, cu_seqlens=d["cu"])
+    for m in (*NAMES, "initial_state"):
+        check(got[m], gr[m], got[m].dtype, "d" + m, 2)
+        if m != "initial_state":
+            assert not got[m][:, :cu[0]].any() and not got[m][:, cu[-1]:].any()

@@ -42,7 +42,8 @@ __host__ __device__ constexpr int tp_rows(int ks) { return (kC - 16 * ks) * 16; 
 __host__ __device__ constexpr int tp_group(int ks) { return 2 * tp_rows(ks); }         // bytes of a column group
 constexpr int kFacBytes = 2 * kC * 4;          // e^G and beta e^(G_C - G)
 constexpr int kUnitBytes = kTpBytes + kFacBytes;   // workspace of one chunk and value head
-constexpr uint32_t kSpinLimit = 1u << 22;
+constexpr uint32_t kSpinLimit = 1u << 22;      // polls of a wait
+constexpr uint32_t kDrainLimit = 1u << 16;     // of a wait for what is in flight at a block's end
 
 // parts that an input of the type is exactly the sum of (float: to 24 bits)
 template <typename T> struct Parts { static constexpr int n = 3; };
@@ -361,6 +362,31 @@ __device__ __forceinline__ void load_image(unsigned char *dst, int part, int gro
 #pragma unroll
                 for (int i = 0; i < NB; ++i) *reinterpret_cast<uint4 *>(d + i * part + 4 * n * group) = v[n][i];
         }
+    }
+}
+
+// Waits that run out. A wait may run out for some lanes of a warp only, but
+// tensor-memory loads, elect and barriers need them all: so a lane notes it and
+// goes on, over what is not there, and whole warps ask all_ok once a chunk,
+// where they wait anyway, and leave together. Until then no warp whose wait ran
+// out hands a stage back. (Asking behind every wait cost 1 to 3% of the chains.)
+__device__ __forceinline__ void try_wait(bool &ok, uint64_t *m, uint32_t parity) {
+    ok = umma::mbar_wait(m, parity, kSpinLimit) && ok;
+}
+__device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+// `count` copies went to `stages` stages in turn: the parity of the last one's
+// phase in stage i, -1 where there is none
+__host__ __device__ constexpr int last_parity(int count, int stages, int i) {
+    return count > i ? (count - 1 - i) / stages & 1 : -1;
+}
+// Waits for the last copies of a block (its readers have, unless a wait ran
+// out), by the threads that issued them.
+__device__ __forceinline__ void drain_copies(uint64_t *full, int count, int stages) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int i = 0; i < stages; ++i) {
+        const int parity = last_parity(count, stages, i);
+        if (parity >= 0) umma::mbar_wait(full + i, parity, kDrainLimit);
     }
 }
 

@@ -28,7 +28,7 @@ using namespace delta;
 //   kTmX   the parts of dO (64 columns), low kTmXl; later those of scale e^G dO
 constexpr int kTmS = 0, kTmSl = 128, kTmK = 192, kTmR = 256, kTmX = 320, kTmKl = 384, kTmRl = 416, kTmXl = 448;
 
-enum { bFull = 0, bEmpty = 2, bS = 4, bK = 8, bR = 10, bX = 12, bY, bM1, bMx, bM2, bM3, bCount };
+enum { bFull = 0, bEmpty = 2, bS = 4, bK = 8, bR = 10, bX = 12, bY, bM1, bMx, bM2, bM3, bEnd, bCount };
 
 // SUM: dN of a segment, the state's gradient before it from none behind it,
 // without output. Otherwise the segment itself, from the gradient behind it.
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
             umma::mbar_init(bars + bEmpty + i, 1 + kEpiWarps);
         }
         for (int i = bS; i <= bY; ++i) umma::mbar_init(bars + i, kEpiWarps);
-        for (int i = bM1; i <= bM3; ++i) umma::mbar_init(bars + i, 1);
+        for (int i = bM1; i <= bEnd; ++i) umma::mbar_init(bars + i, 1);
         umma::fence_mbar_init();
     }
     umma::fence_before_sync();
@@ -70,12 +70,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
     umma::fence_after_sync();
     const uint32_t tm = uniform(*tslot);
     bool ok = true;
+    int issued = 0;   // chunks on their way, of the loading threads
 
     if (warp > kEpiWarps) {
         // ------------------------------------------------------ loading ----
         const int lt = tid - (kEpiWarps + 1) * 32;
-        for (int n = 0, st = 0, turn = 0; n < chunks; ++n) {
-            const int c = chunks - 1 - n;
+        for (int st = 0, turn = 0; issued < chunks; ++issued) {
+            const int c = chunks - 1 - issued;
             const long long slot = sq.slot0 + c;
             const unsigned char *up = ws + (size_t)(slot * a.hv + hv) * kUnitBytes;
             const unsigned char *ip = images + (size_t)(slot * a.hk + hk) * L::kTp;
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
             if (c > 0)
                 prefetch_stage<T, DKT>(ip - (size_t)a.hk * L::kTp, up - (size_t)a.hv * kUnitBytes, op - kC * orow, orow,
                                        kC, a.dv, lt);
-            ok = umma::mbar_wait(bars + bEmpty + st, (turn & 1) ^ 1, kSpinLimit);   // the first use needs no wait
+            try_wait(ok, bars + bEmpty + st, (turn & 1) ^ 1);   // the first use needs no wait
             if (!ok) break;
             load_stage<T, DKT>(smem + st * stage_bytes, ip, up, op, orow, sq.len - c * kC, a.dv, lt, bars + bFull + st);
             if (++st == ST) {
@@ -91,13 +92,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 ++turn;
             }
         }
-        // every copy has been waited for by the readers, unless a wait ran out: then here
-        if (!ok)
-            for (int i = 0; i < ST; ++i) umma::mbar_wait(bars + bFull + i, 0, 1u << 16);
     } else if (warp == kEpiWarps) {
         // ----------------------------------------------------- products ----
         const uint32_t base = saddr(smem);
-        for (int n = 0, st = 0, turn = 0; n < chunks && ok; ++n) {
+        for (int n = 0, st = 0, turn = 0; n < chunks && all_ok(ok); ++n) {
             const int pn = n & 1;
             const uint32_t k0 = base + st * stage_bytes, t0 = k0 + L::kTp;
             // columns 16 ks of dR^T (+)= part p of operand (at, low), K step ib, times part j of T (pt = 0) or PT (1)
@@ -107,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                                tp_group(ks)),
                        idesc(16, false, true), acc);
             };
-            ok = umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit);
+            try_wait(ok, bars + bFull + st, turn & 1);
             // D1 = dS1^T K^T, steps m and NS + m; the orders of the parts' products as in the forward chain
             auto state_times = [&](int m, int most, int least) {
 #pragma unroll
@@ -125,9 +123,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
             };
 #pragma unroll
             for (int m = 0; m < NS; ++m) {
-                ok = ok && umma::mbar_wait(bars + bS + m, pn, kSpinLimit);
+                try_wait(ok, bars + bS + m, pn);
                 umma::fence_after_sync();
-                if (ok && elect()) {
+                if (elect()) {
                     state_times(m, 2, 1);
                     if (m == NS - 1) {
 #pragma unroll
@@ -138,9 +136,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 __syncwarp();
             }
             // dR^T = dO^T PT + ..
-            ok = ok && umma::mbar_wait(bars + bX, pn, kSpinLimit);
+            try_wait(ok, bars + bX, pn);
             umma::fence_after_sync();
-            if (ok && elect()) {
+            if (elect()) {
 #pragma unroll
                 for (int o = 2; o >= 0; --o)
 #pragma unroll
@@ -156,9 +154,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
             // .. + (beta e^(G_C - G) D1) T
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                ok = ok && umma::mbar_wait(bars + bK + m, pn, kSpinLimit);
+                try_wait(ok, bars + bK + m, pn);
                 umma::fence_after_sync();
-                if (ok && elect()) {
+                if (elect()) {
                     auto group = [&](int first, int most, int least) {
 #pragma unroll
                         for (int o = most; o >= least; --o)
@@ -191,17 +189,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                                !first || o < 2 || j > 0);
                     }
             };
-            ok = ok && umma::mbar_wait(bars + bY, pn, kSpinLimit) && umma::mbar_wait(bars + bM1, pn, kSpinLimit);
+            try_wait(ok, bars + bY, pn);
+            try_wait(ok, bars + bM1, pn);
             umma::fence_after_sync();
-            if (ok && elect())
+            if (elect())
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) tok_times(kTmX, kTmXl, kC, ks, ks == 0, 2, 1);
             __syncwarp();
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                ok = ok && umma::mbar_wait(bars + bR + m, pn, kSpinLimit);
+                try_wait(ok, bars + bR + m, pn);
                 umma::fence_after_sync();
-                if (ok && elect()) {
+                if (elect()) {
                     tok_times(kTmR, kTmRl, 0, m, false, 2, 1);
                     tok_times(kTmR, kTmRl, 0, 2 + m, false, 2, 1);
                     if (m == 1) {
@@ -211,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                             tok_times(kTmR, kTmRl, 0, ks, false, 0, 0);
                         }
                         umma::commit(bars + bM3);
-                        umma::commit(bars + bEmpty + st);
+                        if (n + ST < chunks) umma::commit(bars + bEmpty + st);
                     }
                 }
                 __syncwarp();
@@ -256,8 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 done(bS + m);
             }
             if (!SUM && vin) store_state<HC>(keep_ds + (size_t)unit * a.dk * a.dv, S, h, v, a.dk, a.dv);
-            ok = umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit);
-            if (!ok) break;
+            try_wait(ok, bars + bFull + st, turn & 1);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {   // dO^T
                 const int j0 = h * (kC / 2) + 16 * m;
@@ -267,8 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 tm_parts16<NB>(mine + kTmX + j0, mine + kTmXl + j0 / 2, x);
             }
             done(bX);
-            ok = umma::mbar_wait(bars + bM1, pn, kSpinLimit);
-            if (!ok) break;
+            try_wait(ok, bars + bM1, pn);
             umma::fence_after_sync();
 #pragma unroll
             for (int m = 0; m < 2; ++m) {   // beta e^(G_C - G) D1
@@ -281,8 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 tm_split16(mine + kTmK + j0, mine + kTmKl + j0 / 2, x);
                 done(bK + m);
             }
-            ok = umma::mbar_wait(bars + bMx, pn, kSpinLimit);
-            if (!ok) break;
+            try_wait(ok, bars + bMx, pn);
             umma::fence_after_sync();
 #pragma unroll
             for (int m = 0; m < 2; ++m) {   // scale e^G dO^T, in the place of dO^T
@@ -294,8 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 tm_split16(mine + kTmX + j0, mine + kTmXl + j0 / 2, x);
             }
             done(bY);
-            ok = umma::mbar_wait(bars + bM2, pn, kSpinLimit);
-            if (!ok) break;
+            try_wait(ok, bars + bM2, pn);
             umma::fence_after_sync();
 #pragma unroll
             for (int m = 0; m < 2; ++m) {   // dR^T = dV^T, and -e^G dR as the next operand
@@ -314,10 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                            rows - j0);
             }
             const float total = eg[kC - 1];   // e^(G_C): rows past the end have g = 0
-            __syncwarp();
+            if (!all_ok(ok)) break;
             if (lane == 0) mbar_arrive(bars + bEmpty + st);
-            ok = umma::mbar_wait(bars + bM3, pn, kSpinLimit);
-            if (!ok) break;
+            try_wait(ok, bars + bM3, pn);
             umma::fence_after_sync();
 #pragma unroll
             for (int i = 0; i < HC; i += 16) {
@@ -338,15 +332,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 if (h * HC + i < a.dk) to[(size_t)(h * HC + i) * a.dv] = S[i];
         }
     }
-    if (!ok && flags && lane == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
-    if (warp == kEpiWarps && !ok) {   // a wait that ran out may leave products in flight
-        if (lane == 0) umma::commit(bars + bM3);
-        __syncwarp();
-        umma::mbar_wait(bars + bM3, 0, 1u << 16);
-        umma::mbar_wait(bars + bM3, 1, 1u << 16);
-    }
+    if (!ok && flags) atomicOr(flags, S4_FLAG_TIMEOUT);
     umma::fence_before_sync();
-    __syncthreads();
+    if (__syncthreads_or(!ok)) {   // a wait ran out: what is still under way ends before its memory goes
+        if (warp > kEpiWarps) drain_copies(bars + bFull, issued, ST);
+        if (warp == kEpiWarps) {
+            if (elect()) umma::commit(bars + bEnd);
+            __syncwarp();
+            umma::mbar_wait(bars + bEnd, 0, kDrainLimit);
+        }
+        __syncthreads();
+    }
     umma::fence_after_sync();
     if (warp == 0) umma::tmem_dealloc(tm, 512);
 }

@@ -38,7 +38,7 @@ using namespace delta;
 //   kTmQ, kTmO   S0^T Q^T and (PT R)^T (64 each)
 constexpr int kTmS = 0, kTmSl = 128, kTmK = 192, kTmE = 256, kTmQ = 320, kTmO = 384, kTmRl = 448, kTmEl = 480;
 
-enum { bFull = 0, bEmpty = 2, bS = 4, bR = 8, bE = 10, bO = 12, bM1, bM2, bMq, bM2o, bM3, bCount };
+enum { bFull = 0, bEmpty = 2, bS = 4, bR = 8, bE = 10, bO = 12, bM1, bM2, bMq, bM2o, bM3, bEnd, bCount };
 
 // SUM: what a segment does to the state, S -> M S + N, without output: blocks
 // 2 b write N (the segment from a zero state), blocks 2 b + 1 M (without V,
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
             umma::mbar_init(bars + bEmpty + i, 1 + kEpiWarps);
         }
         for (int i = bS; i <= bO; ++i) umma::mbar_init(bars + i, kEpiWarps);
-        for (int i = bM1; i <= bM3; ++i) umma::mbar_init(bars + i, 1);
+        for (int i = bM1; i <= bEnd; ++i) umma::mbar_init(bars + i, 1);
         umma::fence_mbar_init();
     }
     umma::fence_before_sync();
@@ -88,11 +88,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
     umma::fence_after_sync();
     const uint32_t tm = uniform(*tslot);
     bool ok = true;
+    int issued = 0;   // chunks on their way, of the loading threads
 
     if (warp > kEpiWarps) {
         // ------------------------------------------------------ loading ----
         const int lt = tid - (kEpiWarps + 1) * 32;
-        for (int c = 0, st = 0, turn = 0; c < chunks; ++c) {
+        for (int st = 0, turn = 0; issued < chunks; ++issued) {
+            const int c = issued;
             const long long slot = sq.slot0 + c;
             const unsigned char *up = ws + (size_t)(slot * a.hv + hv) * kUnitBytes;
             const unsigned char *ip = images + (size_t)(slot * a.hk + hk) * L::kTp;
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
             if (c + 1 < chunks)
                 prefetch_stage<T, DKT>(ip + (size_t)a.hk * L::kTp, up + (size_t)a.hv * kUnitBytes, vp + kC * a.sv, a.sv,
                                        sq.len - (c + 1) * kC, a.dv, lt);
-            ok = umma::mbar_wait(bars + bEmpty + st, (turn & 1) ^ 1, kSpinLimit);   // the first use needs no wait
+            try_wait(ok, bars + bEmpty + st, (turn & 1) ^ 1);   // the first use needs no wait
             if (!ok) break;
             load_stage<T, DKT>(smem + st * stage_bytes, ip, up, vp, a.sv, sq.len - c * kC, a.dv, lt, bars + bFull + st);
             if (++st == ST) {
@@ -108,16 +110,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 ++turn;
             }
         }
-        // every copy has been waited for by the readers, unless a wait ran out: then here
-        if (!ok)
-            for (int i = 0; i < ST; ++i) umma::mbar_wait(bars + bFull + i, 0, 1u << 16);
     } else if (warp == kEpiWarps) {
         // ----------------------------------------------------- products ----
         // A K step's products start as soon as the threads have written its
         // parts. What the next step waits for goes first, Q's and PT's products
         // into the gaps.
         const uint32_t base = saddr(smem);
-        for (int c = 0, st = 0, turn = 0; c < chunks && ok; ++c) {
+        for (int c = 0, st = 0, turn = 0; c < chunks && all_ok(ok); ++c) {
             const int pc = c & 1;
             const uint32_t k0 = base + st * stage_bytes, t0 = k0 + L::kTp;
             // Of every product the orders from `most` to `least` (2: the smallest
@@ -167,13 +166,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                                    n + h > 0 || o < 2 || j > 0);
                         }
             };
-            ok = umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit) &&
-                 (c == 0 || umma::mbar_wait(bars + bM2o, pc ^ 1, kSpinLimit));   // R's parts have been read
+            try_wait(ok, bars + bFull + st, turn & 1);
+            if (c > 0) try_wait(ok, bars + bM2o, pc ^ 1);   // R's parts have been read
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
-                ok = ok && umma::mbar_wait(bars + bS + n, pc, kSpinLimit);
+                try_wait(ok, bars + bS + n, pc);
                 umma::fence_after_sync();
-                if (ok && elect()) {
+                if (elect()) {
                     state_times(kTmK, 0, n, 2, 1);
                     if (n == NS - 1) {
 #pragma unroll
@@ -184,18 +183,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 __syncwarp();
             }
             if constexpr (!SUM) {
-                ok = ok && (c == 0 || umma::mbar_wait(bars + bO, pc ^ 1, kSpinLimit));   // the last output's terms have been read
+                if (c > 0) try_wait(ok, bars + bO, pc ^ 1);   // the last output's terms have been read
                 umma::fence_after_sync();
-                if (ok && elect())
+                if (elect())
 #pragma unroll
                     for (int n = 0; n < NS; ++n) state_times(kTmQ, kC, n, 2, 1);
                 __syncwarp();
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                ok = ok && umma::mbar_wait(bars + bR + n, pc, kSpinLimit);
+                try_wait(ok, bars + bR + n, pc);
                 umma::fence_after_sync();
-                if (ok && elect()) {
+                if (elect()) {
                     r_times(kTmE, 0, n, 2, 1);
                     if (n == 1) {
                         r_times(kTmE, 0, 0, 0, 0);
@@ -212,10 +211,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                ok = ok && umma::mbar_wait(bars + bE + n, pc, kSpinLimit);
-                if (n == 0) ok = ok && umma::mbar_wait(bars + bMq, pc, kSpinLimit);   // the state's parts have been read
+                try_wait(ok, bars + bE + n, pc);
+                if (n == 0) try_wait(ok, bars + bMq, pc);   // the state's parts have been read
                 umma::fence_after_sync();
-                if (ok && elect()) {
+                if (elect()) {
                     e_times(n, 2, 1);
                     if (n == 1) {
                         e_times(0, 0, 0);
@@ -228,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                             r_times(kTmO, 1, 1, 0, 0);
                         }
                         umma::commit(bars + bM2o);
-                        umma::commit(bars + bEmpty + st);
+                        if (c + ST < chunks) umma::commit(bars + bEmpty + st);
                     }
                 }
                 __syncwarp();
@@ -275,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
         auto put_output = [&](int c, int st) {
             const int rows = sq.len - c * kC < kC ? sq.len - c * kC : kC;
             const float *eg = reinterpret_cast<const float *>(smem + st * stage_bytes + L::kTp + kTpBytes);
-            ok = umma::mbar_wait(bars + bM2o, c & 1, kSpinLimit) && ok;
+            try_wait(ok, bars + bM2o, c & 1);
             umma::fence_after_sync();
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
@@ -307,9 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
             const long long unit = (sq.slot0 + c) * a.hv + hv;
             if (!SUM && keep_s && vin) store_state<HC>(keep_s + (size_t)unit * a.dk * a.dv, S, h, v, a.dk, a.dv);
             if (!SUM && c > 0) put_output(c - 1, before);
-            ok = ok && umma::mbar_wait(bars + bFull + st, turn & 1, kSpinLimit) &&
-                 umma::mbar_wait(bars + bM1, pc, kSpinLimit);
-            if (!ok) break;
+            try_wait(ok, bars + bFull + st, turn & 1);
+            try_wait(ok, bars + bM1, pc);
             umma::fence_after_sync();
 #pragma unroll
             for (int n = 0; n < 2; ++n) {   // R^T = V^T - e^G S0^T K^T
@@ -324,8 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 tm_split16(mine + kTmK + j0, mine + kTmRl + j0 / 2, x);
                 done(bR + n);
             }
-            ok = umma::mbar_wait(bars + bM2, pc, kSpinLimit);
-            if (!ok) break;
+            try_wait(ok, bars + bM2, pc);
             umma::fence_after_sync();
 #pragma unroll
             for (int n = 0; n < 2; ++n) {   // E^T, and beta e^(G_C - G) E as the next operand
@@ -340,12 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                 done(bE + n);
             }
             const float total = eg[kC - 1];   // e^(G_C): rows past the end have g = 0
-            if (SUM) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars + bEmpty + st);
-            }
-            ok = umma::mbar_wait(bars + bM3, pc, kSpinLimit);
-            if (!ok) break;
+            if (!all_ok(ok)) break;
+            if (SUM && lane == 0) mbar_arrive(bars + bEmpty + st);
+            try_wait(ok, bars + bM3, pc);
             umma::fence_after_sync();
 #pragma unroll
             for (int i = 0; i < HC; i += 16) {
@@ -362,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
             }
         }
         if constexpr (SUM) {
+            if (chunks) try_wait(ok, bars + bM2o, (chunks - 1) & 1);   // its arrival, which only a next chunk waits for
             float *to = ident ? su.m(sums, block) + (size_t)v * a.dk : su.n(sums, block) + v;
             float *rows = ident && keep_m ? su.m_rows(sums, block) + v : nullptr;
             if (vin)
@@ -372,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
                         if (rows) rows[(size_t)(h * HC + i) * a.dk] = S[i];
                     }
         } else {
-            if (ok && chunks) put_output(chunks - 1, before);
+            if (chunks && all_ok(ok)) put_output(chunks - 1, before);
             if (last && sg.last && vin) {
 #pragma unroll
                 for (int i = 0; i < HC; ++i)
@@ -380,15 +375,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_forward(DeltaArgs a, cons
             }
         }
     }
-    if (!ok && flags && lane == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
-    if (warp == kEpiWarps && !ok) {   // a wait that ran out may leave products in flight
-        if (lane == 0) umma::commit(bars + bM3);
-        __syncwarp();
-        umma::mbar_wait(bars + bM3, 0, 1u << 16);
-        umma::mbar_wait(bars + bM3, 1, 1u << 16);
-    }
+    if (!ok && flags) atomicOr(flags, S4_FLAG_TIMEOUT);
     umma::fence_before_sync();
-    __syncthreads();
+    if (__syncthreads_or(!ok)) {   // a wait ran out: what is still under way ends before its memory goes
+        if (warp > kEpiWarps) drain_copies(bars + bFull, issued, ST);
+        if (warp == kEpiWarps) {
+            if (elect()) umma::commit(bars + bEnd);
+            __syncwarp();
+            umma::mbar_wait(bars + bEnd, 0, kDrainLimit);
+        }
+        __syncthreads();
+    }
     umma::fence_after_sync();
     if (warp == 0) umma::tmem_dealloc(tm, 512);
 }

@@ -28,3 +28,10 @@ def test_shared_memory_limit_from_two_threads(tmp_path, flags):
 
 def test_resident_blocks_from_four_threads(tmp_path):
     run(tmp_path, "resident.cpp", "-fsanitize=thread")
+
+
+def test_the_last_copy_of_every_stage_is_waited_for(tmp_path):
+    exe = str(tmp_path / "program")
+    subprocess.run([s4build._nvcc(), *s4build.NVCC_FLAGS, os.path.join(HOST, "last_parity.cu"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr

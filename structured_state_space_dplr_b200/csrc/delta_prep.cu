@@ -89,7 +89,8 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
     float2 *Gs = reinterpret_cast<float2 *>(smem + L::kBig);
     float *cs = reinterpret_cast<float *>(Gs + kC), *bs = cs + kC, *ds = bs + kC, *rs = ds + kC;
     uint64_t *bar = reinterpret_cast<uint64_t *>(rs + kC);
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 1);
+    uint64_t *done = bar + 1;   // for the block's end
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 2);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
     const long long slot = blockIdx.x / a.hv;
@@ -105,6 +106,7 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
     if (warp == 0) umma::tmem_alloc(tslot, 128);
     if (tid == 0) {
         umma::mbar_init(bar, 1);
+        umma::mbar_init(done, 1);
         umma::fence_mbar_init();
     }
     if (warp == 1) {
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
 #pragma unroll 4
         for (int n = tid; n < kq_bytes<T, DKT>() / 16; n += 256) dst[n] = reinterpret_cast<const uint4 *>(smem)[n];
     }
-    ok = umma::mbar_wait(bar, 0, kSpinLimit);
+    try_wait(ok, bar, 0);
     umma::fence_after_sync();
     const uint32_t mine = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const int i = tid & (kC - 1), ib = i >> 4;   // this thread's row, and its 16 tokens
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
             }
             __syncwarp();
         }
-        ok = umma::mbar_wait(bar, 1 ^ pass, kSpinLimit) && ok;
+        try_wait(ok, bar, 1 ^ pass);
         umma::fence_after_sync();
         if (is_p) {
             float d[16];
@@ -360,7 +362,12 @@ __global__ void __launch_bounds__(256, PrepSmem<T, DKT>::kBytes < 57000 ? 4 : Pr
                 }
         }
     }
-    if (!ok && flags && tid == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
+    if (!ok && flags) atomicOr(flags, S4_FLAG_TIMEOUT);
+    if (warp == 0 && !all_ok(ok)) {   // the products' own warp has not seen the last ones done
+        if (elect()) umma::commit(done);
+        __syncwarp();
+        umma::mbar_wait(done, 0, kDrainLimit);
+    }
     umma::fence_before_sync();
     __syncthreads();
     if (warp == 0) umma::tmem_dealloc(tm, 128);

@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(kGradBlock, 1)
     float *gsum = csum + 4 * kC, *rsum = gsum + 4 * kC;                      // [4][64], [128]
     float *dot = rsum + 2 * kC, *hdot = dot + 4 * kC;                        // [2][128], [2][64]
     float *red = hdot + 2 * kC;                                              // [8]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(red + 8);                  // kq, two products in flight, raw
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 4);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(red + 8);                  // kq, two products in flight, raw, end
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 5);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int R = (warp & 3) * 32 + lane, i = R & (kC - 1), half = warp >> 2;   // row of [dR; dO] and of [K; Q], its token
     const bool low = R < kC;                                                    // a row of dR and K
@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kGradBlock, 1)
     if (tid == 0) {
         for (int n = 0; n < 3; ++n) umma::mbar_init(bars + n, 1);
         umma::mbar_init(bars + 3, kGradThreads + 1);
+        umma::mbar_init(bars + 4, 1);
         umma::fence_mbar_init();
     }
     umma::fence_before_sync();
@@ -181,29 +182,32 @@ __global__ void __launch_bounds__(kGradBlock, 1)
     const uint32_t tm = uniform(*tslot);
     const uint32_t mine = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s0 = saddr(smem), kq0 = saddr(kq), e0 = saddr(ei);
-    int kq_turn = 0, turn1 = 0, turn2 = 0;
+    int kq_turn = 0, kq_loads = 0, raw_loads = 0, turn1 = 0, turn2 = 0;
     bool ok = true;
     auto load_kq = [&]() {   // behind a barrier of the block; every thread waits
-        if (tid == 0) {
+        if (ok && tid == 0) {
             mbar_expect(bars, L::kKq);
             bulk_load(kq, images + (size_t)(slot * a.hk + hk) * L::kKq, L::kKq, bars);
             mbar_arrive(bars);
+            ++kq_loads;
         }
-        ok = umma::mbar_wait(bars, kq_turn++ & 1, kSpinLimit) && ok;
+        try_wait(ok, bars, kq_turn++ & 1);
     };
-    auto barrier = [&]() {   // operands written by these threads before, products (and bulk loads) behind
+    // operands written by these threads before, products (and bulk loads) behind;
+    // a wait that ran out anywhere is known everywhere, and nothing more is issued
+    auto barrier = [&]() {
         tm_wait_st();
         umma::fence_proxy_async();
         umma::fence_before_sync();
-        __syncthreads();
+        ok = __syncthreads_and(ok);
         umma::fence_after_sync();
     };
     auto wait1 = [&]() {
-        ok = umma::mbar_wait(bars + 1, turn1++ & 1, kSpinLimit) && ok;
+        try_wait(ok, bars + 1, turn1++ & 1);
         umma::fence_after_sync();
     };
     auto wait2 = [&]() {
-        ok = umma::mbar_wait(bars + 2, turn2++ & 1, kSpinLimit) && ok;
+        try_wait(ok, bars + 2, turn2++ & 1);
         umma::fence_after_sync();
     };
     // D (+)= A [parts of K = 16 KS columns] times an image's PB parts
@@ -250,7 +254,8 @@ __global__ void __launch_bounds__(kGradBlock, 1)
         __syncwarp();
         // E and dR as they are to the place of the states' image, when nobody reads it
         auto load_raw = [&](int g) {
-            if (elect()) {
+            if (elect() && ok) {
+                ++raw_loads;
                 const long long unit = slot * a.hv + hk * per + g;
                 const uint32_t bytes = (uint32_t)(kC * a.dv) * 4;
                 mbar_expect(bars + 3, 2 * bytes);
@@ -263,6 +268,7 @@ __global__ void __launch_bounds__(kGradBlock, 1)
         if (L::kBeside) load_raw(0);
         for (int g = 0; g < per; ++g) {
             barrier();
+            if (!ok) break;
             if (!L::kBeside) load_raw(g);
             barrier();
             if (elect()) {
@@ -285,7 +291,7 @@ __global__ void __launch_bounds__(kGradBlock, 1)
             }
             __syncwarp();
             if (L::kBeside && g + 1 < per) {
-                ok = umma::mbar_wait(bars + 1, 0, kSpinLimit) && ok;   // the phases' products: q.k, then X F and H in turn
+                try_wait(ok, bars + 1, 0);   // the phases' products: q.k, then X F and H in turn
                 load_raw(g + 1);
             }
             if constexpr (!L::kBeside) {
@@ -302,6 +308,11 @@ __global__ void __launch_bounds__(kGradBlock, 1)
             __syncwarp();
             __syncthreads();
         }
+        // the last products are done before the memory that they use goes, and the copies that nobody waits for any more
+        if (elect()) umma::commit(bars + 4);
+        __syncwarp();
+        umma::mbar_wait(bars + 4, 0, kDrainLimit);
+        if (!ok) drain_copies(bars + 3, raw_loads, 1);
     } else {
     // q_i.k_j and k_i.k_j, the same for all value heads
     load_kq();
@@ -319,6 +330,7 @@ __global__ void __launch_bounds__(kGradBlock, 1)
     for (int n = 0; n < HK; ++n) acc[n] = 0.0f;
 
     auto load_do = [&](int g) {   // dO's rows, padded, zeros behind the last
+        if (!ok) return;
         constexpr int E = 16 / (int)sizeof(T), kPer = DVT / E;
         const T *src = dout + tok * orow + (long long)(hk * per + g) * a.dv;
         for (int n = tid; n < kC * kPer; n += kGradThreads) {
@@ -334,6 +346,7 @@ __global__ void __launch_bounds__(kGradBlock, 1)
         const long long unit = slot * a.hv + hv;
         const float *us = keep_s + (size_t)unit * a.dk * a.dv, *ud = keep_ds + (size_t)unit * a.dk * a.dv;
         barrier();   // the last head's reads of shared and tensor memory
+        if (!ok) break;
         if (!L::kBeside) load_do(g);
         if (warp == 1) {
             const GateSums gt = gate_sums(a, tok, hv, rows, lane);
@@ -361,7 +374,7 @@ __global__ void __launch_bounds__(kGradBlock, 1)
         }
         float f[4][8];
         get_state<DKT, DVT>(f, 0, us, a.dk, a.dv, tid);   // on its way
-        ok = umma::mbar_wait(bars + 3, g & 1, kSpinLimit) && ok;
+        try_wait(ok, bars + 3, g & 1);
         // E as right operand (rows tokens, K = v)
 #pragma unroll
         for (int u = 0; u < kC * DVT / 8 / kGradThreads; ++u) {
@@ -585,6 +598,7 @@ __global__ void __launch_bounds__(kGradBlock, 1)
             for (int t = 0; t < 16; ++t) acc[n + t] += x[t];
         }
     }
+    if (!ok) drain_copies(bars, kq_loads, 1);
     if (i < rows) {
         T *o = (low ? dk : dq) + ((tok + i) * a.hk + hk) * a.dk + half * HK;
 #pragma unroll
@@ -601,7 +615,7 @@ __global__ void __launch_bounds__(kGradBlock, 1)
             }
     }
     }
-    if (!ok && flags && lane == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
+    if (!ok && flags) atomicOr(flags, S4_FLAG_TIMEOUT);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();

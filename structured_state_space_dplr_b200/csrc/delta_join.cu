@@ -36,7 +36,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(DeltaArgs a, const 
     const long long first = segment0(a, s);
     const bool in = r0 < a.dk && v0 + c0 < a.dv;   // dk and dv are multiples of 8
     auto unit = [&](int g) { return (size_t)((first + (BACK ? n - 1 - g : g)) * a.hv + hv); };
+    int fetched = 0;
     auto fetch = [&](int g) {   // by one thread
+        ++fetched;
         umma::fence_proxy_async();
         mbar_expect(full + (g & 1), mm * 4);
         bulk_load(Ms + (g & 1) * mm, BACK ? su.m_rows(sums, unit(g)) : su.m(sums, unit(g)), mm * 4, full + (g & 1));
@@ -71,27 +73,37 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(DeltaArgs a, const 
         for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(&S[r0 + j][c0]) = x[j];
         __syncthreads();   // S is there; the other half of Ms is used up
         if (threadIdx.x == 0 && g + 2 < n) fetch(g + 1);
-        ok = umma::mbar_wait(full + (g & 1), (g >> 1) & 1, kSpinLimit) && ok;
+        ok = umma::mbar_wait(full + (g & 1), (g >> 1) & 1, kSpinLimit);
         if (in) {
             const float *M = Ms + (g & 1) * mm + r0;
             const int columns = BACK || g > 0 || init ? a.dk : 0;   // the first M is not there for a state of zeros
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[j] = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-            for (int c = 0; c < columns; ++c) {
-                const float4 m = *reinterpret_cast<const float4 *>(M + c * a.dk);
-                const float4 u = *reinterpret_cast<const float4 *>(&S[c][c0]);
-                x[0] = fma4(m.x, u, x[0]);
-                x[1] = fma4(m.y, u, x[1]);
-                x[2] = fma4(m.z, u, x[2]);
-                x[3] = fma4(m.w, u, x[3]);
+            for (int c = 0; c < columns; c += 8) {   // dk is a multiple of 8
+                float4 m[8], u[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    m[k] = *reinterpret_cast<const float4 *>(M + (c + k) * a.dk);
+                    u[k] = *reinterpret_cast<const float4 *>(&S[c + k][c0]);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    x[0] = fma4(m[k].x, u[k], x[0]);
+                    x[1] = fma4(m[k].y, u[k], x[1]);
+                    x[2] = fma4(m[k].z, u[k], x[2]);
+                    x[3] = fma4(m[k].w, u[k], x[3]);
+                }
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[j] = fma4(1.0f, p[j], x[j]);
         }
-        __syncthreads();
+        if (!__syncthreads_and(ok)) {
+            ok = false;
+            break;
+        }
     }
-    if (!ok && flags && threadIdx.x == 0) atomicOr(flags, S4_FLAG_TIMEOUT);
+    if (!ok && threadIdx.x == 0) drain_copies(full, fetched, 2);
+    if (!ok && flags) atomicOr(flags, S4_FLAG_TIMEOUT);
 }
 
 template <bool BACK>

@@ -455,3 +455,43 @@ def test_packed_segments_without_states(cu, dtype, shape):
         check(got[m], gr[m], got[m].dtype, "d" + m, 2)
         if m != "initial_state":
             assert not got[m][:, :cu[0]].any() and not got[m][:, cu[-1]:].any()
+
+
+def test_calls_from_two_threads_in_a_new_process():
+    """Value heads of different sizes, and rows of different lengths, share
+    kernels whose shared memory is asked for by whoever comes first."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = """
+import sys, threading
+sys.path[:0] = [%r, %r]
+import torch
+import structured_state_space_dplr_b200 as s4
+from test_gpu_gated_delta import NAMES, gen
+from test_gpu_gated_delta_scan import make
+cases = [make(1, 70, 1, 2, 128, Dv, "bfloat16") for Dv in (128, 64, 128, 8)]
+x = [torch.randn(40, D, device="cuda", generator=gen(1)).bfloat16() for D in (8192, 520, 4096, 2048)]
+torch.cuda.synchronize()
+start, results = threading.Barrier(4), [[] for _ in cases]
+def run(i):
+    start.wait()
+    for _ in range(20):
+        d = cases[i]
+        o, last, work = s4.gated_delta_forward(*(d[n] for n in NAMES), keep=True)
+        grads = s4.gated_delta_backward(*(d[n] for n in NAMES), d["v"], work)
+        w = torch.ones(x[i].shape[1], device="cuda")
+        z, mean, rstd = s4.layernorm(x[i], w, w)
+        results[i].append((o, last, *grads.values(), z, *s4.layernorm_backward(z, x[i], w, mean, rstd)))
+    torch.cuda.synchronize()
+threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+for r in results:
+    assert len(r) == 20, len(r)
+    assert all(torch.equal(a, b) for one in r for a, b in zip(one, r[0]))
+    assert all(torch.isfinite(a).all() for a in r[0])
+""" % (os.path.dirname(here), here)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -368,8 +368,9 @@ __device__ __forceinline__ void load_image(unsigned char *dst, int part, int gro
 // Waits that run out. A wait may run out for some lanes of a warp only, but
 // tensor-memory loads, elect and barriers need them all: so a lane notes it and
 // goes on, over what is not there, and whole warps ask all_ok once a chunk,
-// where they wait anyway, and leave together. Until then no warp whose wait ran
-// out hands a stage back. (Asking behind every wait cost 1 to 3% of the chains.)
+// where they wait anyway, and leave together. A warp hands a stage back only
+// behind that, when it has seen it filled: no copy is started over one under
+// way. (Asking behind every wait cost 1 to 3% of the chains.)
 __device__ __forceinline__ void try_wait(bool &ok, uint64_t *m, uint32_t parity) {
     ok = umma::mbar_wait(m, parity, kSpinLimit) && ok;
 }

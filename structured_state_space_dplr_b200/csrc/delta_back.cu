@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                 tm_split16(mine + kTmK + j0, mine + kTmKl + j0 / 2, x);
                 done(bK + m);
             }
+            if (!all_ok(ok)) break;
             try_wait(ok, bars + bMx, pn);
             umma::fence_after_sync();
 #pragma unroll
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_backward(DeltaArgs a, con
                            rows - j0);
             }
             const float total = eg[kC - 1];   // e^(G_C): rows past the end have g = 0
-            if (!all_ok(ok)) break;
+            __syncwarp();
             if (lane == 0) mbar_arrive(bars + bEmpty + st);
             try_wait(ok, bars + bM3, pn);
             umma::fence_after_sync();

@@ -182,14 +182,13 @@ __global__ void __launch_bounds__(kGradBlock, 1)
     const uint32_t tm = uniform(*tslot);
     const uint32_t mine = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s0 = saddr(smem), kq0 = saddr(kq), e0 = saddr(ei);
-    int kq_turn = 0, kq_loads = 0, raw_loads = 0, turn1 = 0, turn2 = 0;
+    int kq_turn = 0, raw_loads = 0, turn1 = 0, turn2 = 0;
     bool ok = true;
     auto load_kq = [&]() {   // behind a barrier of the block; every thread waits
         if (ok && tid == 0) {
             mbar_expect(bars, L::kKq);
             bulk_load(kq, images + (size_t)(slot * a.hk + hk) * L::kKq, L::kKq, bars);
             mbar_arrive(bars);
-            ++kq_loads;
         }
         try_wait(ok, bars, kq_turn++ & 1);
     };
@@ -598,7 +597,7 @@ __global__ void __launch_bounds__(kGradBlock, 1)
             for (int t = 0; t < 16; ++t) acc[n + t] += x[t];
         }
     }
-    if (!ok) drain_copies(bars, kq_loads, 1);
+    if (!ok) drain_copies(bars, tid == 0 ? kq_turn : 0, 1);   // (a load left out is waited for in vain, to the limit)
     if (i < rows) {
         T *o = (low ? dk : dq) + ((tok + i) * a.hk + hk) * a.dk + half * HK;
 #pragma unroll

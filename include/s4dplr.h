@@ -663,7 +663,9 @@ s4_status s4_gated_delta_scan(s4_dtype dtype, const void *q, long long q_stride,
  *     sequences may need more, where they run in segments.
  *   d_flags (nullable): S4_FLAG_TIMEOUT if a bounded wait ran out.
  * Operands that are not bf16 are split into bf16 parts (three for float: 24
- * bits) and accumulated in float: results are as good as float arithmetic's.
+ * bits) and accumulated in float, with truncation: float results are off by
+ * about twice what float arithmetic's are (2 to 7e-7 of their norm where that
+ * has 3e-7). Float values above bf16's largest, 3.39e38, count as infinities.
  * A NaN or an infinity in a token's q, k, v or gates makes NaN of what it
  * reaches: later tokens, and earlier ones of the same 64-token chunk (0 times
  * it under the products' masks); never other sequences, or heads that do not

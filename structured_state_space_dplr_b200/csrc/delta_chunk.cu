@@ -17,7 +17,7 @@
 // product starts with the first 16 columns of its operand; Q's and PT's
 // products and the output run in the chain's gaps. A block needs all 512
 // tensor-memory columns, so there is one per SM. Measured: 4 x 4096 tokens, 32
-// heads of 128 bf16 (128 chains of 64 chunks) 250 us, 3.9 us a chunk; 352 us
+// heads of 128 bf16 (128 chains of 64 chunks) 235 us, 3.7 us a chunk; 327 us
 // when the states and E are kept for the backward pass (0.8 GB more to write).
 #include "delta.cuh"
 #include "s4dplr.h"
@@ -425,7 +425,7 @@ cudaError_t run(const DeltaArgs &a, const float *init, float *last, const void *
 // places, H_n / n of them (H_n the harmonic number): 8192 tokens in sequences
 // of 4000, 500, 1000, 692 and four of 500, 8 heads, 314 us in one piece each
 // and 138 in segments; where all have 1024, 88 and 126. One sequence of
-// 65536 tokens, 8 heads of 128: 3515 us for the whole call in one piece, 907
+// 65536 tokens, 8 heads of 128: 3515 us for the whole call in one piece, 890
 // us in 18.
 //
 // A workspace for many tokens has to serve calls with fewer. The best number of

@@ -23,9 +23,11 @@
 // <S0, dS1> then costs the backward chain more than the copies save.) That
 // space allows one block per SM; what bounds it is the chain of conversions and
 // products of a head. Measured: 4 x 4096 tokens, 16 key and 32
-// value heads of 128 bf16 (4096 blocks) 1021 us, 1.9 GB read a time; tensor
-// cores 27%, issue slots 28%. A head's E, dR and dO come to shared memory one
-// head ahead, 1094 us without.
+// value heads of 128 bf16 (4096 blocks) 1013 us, 1.9 GB read a time; tensor
+// cores 28%, issue slots 28%, DRAM 22%. A head's E, dR and dO come to shared
+// memory one head ahead, 1094 us without. Nine warps leave 168 registers a
+// thread, of which heads of 128 spill: 380 bytes in bf16, 436 in half, 368 in
+// float (a variable more alive throughout cost 1.5%).
 #include "delta.cuh"
 #include "s4dplr.h"
 

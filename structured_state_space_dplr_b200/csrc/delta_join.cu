@@ -5,9 +5,12 @@
 //
 // A block has 16 columns of one sequence's and head's state in shared memory, a
 // thread 4 rows and 4 columns of the result: two 16-byte reads for 16 products
-// (one row and 8 columns a thread: 77 us for what takes 53, most of it reads of S). M (by columns going forward, by rows going back: the row index runs
-// over the threads) comes into shared memory one segment ahead. Bound by the
-// segments one after the other. Measured: 65536 tokens, 8 heads of 128 x 128 53 us.
+// (one row and 8 columns a thread: 77 us for what takes 49, most of it reads of
+// S), those of 8 products read before them (left to the compiler 53 to 82 us,
+// with the code around the loop). M (by columns going forward, by rows going
+// back: the row index runs over the threads) comes into shared memory one segment
+// ahead. Bound by the segments one after the other. Measured: 65536 tokens, 8
+// heads of 128 x 128 49 us.
 #include "delta.cuh"
 #include "s4dplr.h"
 

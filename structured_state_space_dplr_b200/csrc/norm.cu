@@ -7,10 +7,13 @@
 //
 // Both directions move each array once (rows: forward x -> z, backward x, dz
 // -> dx; channels: x, dz -> dx). Measured at 32768 rows of 1024 bf16: forward
-// 39 us (3.4 TB/s), backward 50 + 5.5 us (3.6 TB/s), both nearer to the issue
-// rate of their conversions and sums than to memory; 16384 rows of 2048 float,
-// backward: 67 us (6.0 TB/s). Channels, 8 x 256 x 16384: 81 us (4.9 TB/s). The weight gradients are summed in
-// registers over all rows a block visits (a fixed set, in a fixed order),
+// 38 us (3.5 TB/s), backward 49 + 5.5 us (3.7 TB/s). Neither is at a limit: 63
+// and 62% of the issue slots, 27 and 41% of DRAM, 23 and 22% of the warps that
+// an SM holds (registers), which wait for each other's results and for shared
+// memory. 16384 rows of 2048 float, backward: 67 us (6.0 TB/s). Channels, 8 x
+// 256 x 16384: 80 us (5.0 TB/s); above 256 channels 2.7 to 3.0 TB/s, see
+// there. The weight gradients are summed in registers over all rows a block
+// visits (a fixed set, in a fixed order),
 // written as one partial row per block and added up by a second small kernel
 // in a fixed order: no atomics, the same bits every time.
 #include "dtype.cuh"
@@ -110,7 +113,7 @@ struct Weights {
 // ring needs no barrier. With the loads in flight in registers they were paid
 // for in occupancy (32768 rows of 1024 bf16: forward 86 us a row a block, 49 us
 // four rows at a time, 39 us now; backward 74, 117 and 50 us; float rows reach
-// 5.2 and 6.0 TB/s, bf16 ones are bound by their instructions). 8-byte packs:
+// 5.2 and 6.0 TB/s). 8-byte packs:
 // rows that are multiples of 8 bytes only (30000 of 500 bf16, backward: 30 us,
 // as single elements 63). Single elements (V = 1) are loaded where they are used.
 constexpr int kStages = 3;
@@ -578,8 +581,14 @@ __global__ void __launch_bounds__(256) k_layernorm_channels_backward_reg(
 }
 
 // any H: the tile is read three times (mean; variance and the two sums of the
-// gradient; output), the later reads mostly from L2, and the weight gradients
-// are kept in shared memory, each channel's by the slice that owns it
+// gradient; output), dz twice, and the weight gradients are kept in shared
+// memory, each channel's by the slice that owns it. The tiles under way at once
+// are larger than L2 from some 400 channels on (4 blocks an SM, 512 H bytes
+// each), then every read comes from memory: at 4 x 1024 x 8192 670 MB read for
+// 268, 0.2% of them found in L2, 65% of DRAM's rate, the rest waiting for loads
+// that are not started ahead. Measured: 8 x 512 x 16384 300 us, 32 x 1024 x 8192
+// 1076 us, 2.7 and 3.0 TB/s of the 12 bytes an element that have to move; 2 x
+// 4096 x 4096, with 128 tiles fewer blocks than SMs, 429 us.
 __global__ void __launch_bounds__(256) k_layernorm_channels_backward(
     const float *__restrict__ dz, const float *__restrict__ x, const float *__restrict__ gamma, float eps, int Bt,
     int H, int L, float *dx, float *part) {
